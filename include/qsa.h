@@ -316,6 +316,145 @@ qsa_status qsa_sparse_attend_selected_multi(qsa_ctx* ctx, int32_t layer, int32_t
  * by later appends. n_keep >= 0; a larger n_keep than n_ctx changes nothing. */
 qsa_status qsa_rollback(qsa_ctx* ctx, int32_t layer, int32_t n_keep, qsa_stream_t stream);
 
+/* qsa_rollback with the count on the device, for a verification step whose outcome the host
+ * has not seen (a captured step, qsa_verify_drafts): of the n_drafts >= 0 newest tokens the
+ * first *n_accepted stay, i.e. n_keep = n_ctx - n_drafts + *n_accepted. n_accepted is a
+ * device i32; a value outside [0, n_drafts] drops or keeps all drafts and is reported as
+ * device status QSA_ERR_BAD_INDEX. */
+qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, const int32_t* n_accepted,
+                                 qsa_stream_t stream);
+
+/* Verification of drafted tokens against the target's probabilities from given random
+ * numbers (Part 10, section COMMON-004, speaks of speculative decoding; the rule is the
+ * usual one, whose tokens are distributed as the target's own). For each sequence
+ * s < n_seqs, with n = n_drafts[s] drafts d_0..d_{n-1} (n_drafts NULL: max_drafts each):
+ *   draft i is accepted iff every draft before it is and u_i * q_i(d_i) < p_i(d_i);
+ *   m = the number of accepted drafts;
+ *   the next token is drawn with u_last from the weights w_j = max(p_m(j) - q_m(j), 0) if
+ *   m < n, or w_j = p_n(j) if all are accepted: the lowest j with
+ *   w_0 + ... + w_j > u_last * (w_0 + ... + w_{vocab-1}); the last j with w_j > 0 if there
+ *   is none (u_last >= 1), and the lowest j with the largest p_m(j) if no w_j is positive.
+ * Products, differences and sums are taken in 64 bits, in a fixed order.
+ *   target_probs [n_seqs][max_drafts + 1][vocab] f32, rows target_stride floats apart;
+ *   draft_probs  [n_seqs][max_drafts][vocab] f32, rows draft_stride floats apart, or NULL
+ *                for drafts without probabilities (looked up, or the draft model's argmax):
+ *                q_i is then 1 at d_i and 0 elsewhere. A stride of 0 means vocab;
+ *   draft_tokens [n_seqs][max_drafts] i32. An id outside [0, vocab) is rejected, its q_i
+ *                taken as 0 if there are no draft probabilities, and reported;
+ *   n_drafts     [n_seqs] i32 or NULL; a value outside [0, max_drafts] is clamped and reported;
+ *   uniforms     [n_seqs][max_drafts + 1] f32 in [0, 1): u_0.., and u_last in the last place
+ *                whatever n is (a negative number or NaN counts as 0);
+ *   n_accepted, next_token [n_seqs] i32: the outputs.
+ * Probabilities are finite and not negative (weights that are NaN count as 0); they need
+ * not sum to 1. status (may be NULL) is a device i32 that gets QSA_ERR_BAD_INDEX, if it was
+ * 0, where something is reported. Pointers are aligned to their elements. Needs no context;
+ * nothing is written but the outputs and status. 0 <= n_seqs, 0 <= max_drafts <= 64. */
+#define QSA_MAX_DRAFTS 64
+qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                             int64_t draft_stride, const int32_t* draft_tokens, const int32_t* n_drafts,
+                             const float* uniforms, int32_t n_seqs, int32_t max_drafts, int32_t vocab,
+                             int32_t* n_accepted, int32_t* next_token, int32_t* status, qsa_stream_t stream);
+
+/* ---- Paged K/V cache: many sequences, dense attention of their newest tokens ----
+ * The pages compare the sparse path with dense attention, whose time grows with the
+ * context (Part 10, section "なぜFlash Attentionがcontext長に比例していたのか"); up to
+ * indexer_top_k tokens both attend the same cells. These calls serve batches of sequences
+ * that way, from K/V rows held in pages of a pool instead of one buffer a layer. A page
+ * holds page_size consecutive tokens of one sequence; row s of a block table [n_seqs]
+ * [table_width] i32 lists the pages of sequence s in order, so position t of s is place
+ * t % page_size of page block_table[s][t / page_size]. Several sequences may share pages
+ * that none of the calls in flight writes. The calls need no qsa_ctx: they run on the
+ * CURRENT device, which owns every buffer, and report what depends on device data (a page
+ * id outside the pool, a position outside the table) in `status`, a device i32 or NULL
+ * that gets the first code if it was 0. Nothing out of range is read or written. */
+
+/* Storage of a (token, KV head) row of head_dim values in a page.
+ *   QSA_PAGE_F16:  f16 values.
+ *   QSA_PAGE_FP8:  e4m3 codes and one f32 scale = amax * f32(1/448); code = e4m3(x * (448 *
+ *     (1 / amax))) in f32, rounded to nearest even and saturated; an all-zero row has scale 1
+ *     (QSA_KV_FP8 up to the last bit of the factors: one division a row instead of two).
+ *     Value code * scale.
+ *   QSA_PAGE_INT4: groups of 32 dims with one f16 scale s = f16(amax * f32(1/7)); code =
+ *     rint(x * (1 / s)) in f32, clamped to [-7, 7], 0 if s = 0; stored as code + 8 (4 bits).
+ *     Byte j < 16 of a group holds dim j in its low and dim j + 16 in its high half. Value
+ *     f16(code * s), rounded to nearest even. A group that holds a NaN or an infinity
+ *     reads back as NaN. */
+enum { QSA_PAGE_F16 = 0, QSA_PAGE_FP8 = 1, QSA_PAGE_INT4 = 2 };
+
+typedef struct {
+  int32_t n_pages;       /* pages in the pool                                            */
+  int32_t page_size;     /* tokens per page: 16, 32, 64, 128 or 256                      */
+  int32_t n_kv_heads;    /* KV heads                                                     */
+  int32_t head_dim;      /* 64 or 128                                                    */
+  int32_t format;        /* QSA_PAGE_*                                                   */
+  int32_t reserved;      /* 0                                                            */
+  int64_t page_stride;   /* bytes from one page to the next in k_pages and v_pages, a
+                            multiple of 16; 0: the pages follow one another              */
+  int64_t scale_stride;  /* the same in k_scales and v_scales                            */
+  void* k_pages;         /* [n_pages][n_kv_heads][page_size][head_dim] f16, e4m3 bytes, or
+                            [head_dim / 2] bytes of 4-bit codes: a head's rows of a page
+                            are one contiguous piece                                     */
+  void* v_pages;         /* the same                                                     */
+  void* k_scales;        /* QSA_PAGE_FP8: [n_pages][n_kv_heads][page_size] f32; QSA_PAGE_INT4:
+                            [n_pages][n_kv_heads][page_size][head_dim / 32] f16; else NULL */
+  void* v_scales;        /* the same                                                     */
+} qsa_paged_kv;
+
+enum {
+  QSA_PAGED_BUF_PAGES = 0,   /* bytes of k_pages with n_pages pages one after another (v_pages: the same) */
+  QSA_PAGED_BUF_SCALES = 1   /* bytes of k_scales (v_scales: the same); 0 with QSA_PAGE_F16 */
+};
+
+/* Size in bytes of one of a cache's buffers, from its first five fields; 0 if they are invalid. */
+size_t qsa_paged_bytes(const qsa_paged_kv* cache, int32_t which);
+
+/* Stores K/V rows in their pages, quantised to the cache's format.
+ *   k, v [n_rows][n_kv_heads][head_dim] f16, rows row_stride elements apart (0: packed;
+ *   else a multiple of 8, so a slice of a fused projection's output can be passed).
+ *   row_start [n_seqs + 1] i32, ascending: rows row_start[s] .. row_start[s + 1] - 1 belong to
+ *   sequence s and go to its positions first[s], first[s] + 1, ... (first [n_seqs] i32: how
+ *   many tokens the sequence held before). Rows from row_start[n_seqs] on are padding.
+ * Rows outside the table (QSA_ERR_CAPACITY) or with a page id outside the pool
+ * (QSA_ERR_BAD_INDEX) are skipped and reported. Of two rows that go to the same place of the
+ * same page, that place's row is unspecified. */
+qsa_status qsa_paged_write(const qsa_paged_kv* cache, const void* k, const void* v, int64_t row_stride,
+                           int32_t n_rows, const int32_t* block_table, int32_t table_width, int32_t n_seqs,
+                           const int32_t* first, const int32_t* row_start, int32_t* status, qsa_stream_t stream);
+
+/* Reads rows back as f16 values (rounded to nearest even): the arguments of qsa_paged_write,
+ * with k and v as outputs (either may be NULL). Rows that a write would skip come out as
+ * zeros and are reported; padding rows are left as they are. */
+qsa_status qsa_paged_read(const qsa_paged_kv* cache, void* k, void* v, int64_t row_stride, int32_t n_rows,
+                          const int32_t* block_table, int32_t table_width, int32_t n_seqs, const int32_t* first,
+                          const int32_t* row_start, int32_t* status, qsa_stream_t stream);
+
+/* Bytes of the workspace of qsa_paged_attend on the current device, for any number of
+ * sequences of any length; 0 if the arguments are invalid. The workspace holds nothing
+ * between calls and needs no initialisation; calls that may overlap need one each. */
+size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, int32_t n_queries);
+
+/* GQA attention of the n_queries newest tokens of every sequence over all the cells each
+ * of them sees, split over the sequences' lengths and merged.
+ *   q [n_seqs][n_queries][n_q_heads][head_dim] f16, already position-encoded; the
+ *     (sequence, query) rows are q_stride elements apart (0: packed; else a multiple of 8);
+ *   seq_lens [n_seqs] i32: tokens of each sequence in the cache, these newest ones among them;
+ *   query u < n_queries belongs to token seq_lens[s] - n_queries + u and sees the cells up to it:
+ *   out [n_seqs][n_queries][n_q_heads][head_dim] f32 =
+ *     sum_c softmax_c(sm_scale * q_i . K[c][g]) V[c][g], g = i / (n_q_heads / n_kv_heads);
+ *   lse [n_seqs][n_queries][n_q_heads] f32 or NULL: log sum_c exp(sm_scale * q_i . K[c][g]),
+ *     which qsa_cp_merge takes to join parts of a sequence held on several devices.
+ * A query that sees no cell (seq_lens[s] = 0, or fewer tokens than queries) gives out = 0
+ * and lse = -inf. sm_scale 0 means 1/sqrt(head_dim). f32 softmax and accumulation; values of
+ * cells that a query does not see (whatever they hold) do not change its result, and the
+ * result of a sequence does not depend on the others of the batch beyond f32 rounding.
+ * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8. Cells of a page id outside the pool
+ * are skipped (QSA_ERR_BAD_INDEX); a length beyond the table counts as the table's
+ * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). */
+qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_stride, int32_t n_queries,
+                            int32_t n_q_heads, const int32_t* block_table, int32_t table_width, int32_t n_seqs,
+                            const int32_t* seq_lens, float sm_scale, float* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* status, qsa_stream_t stream);
+
 /* ---- Conveniences ---- */
 
 /* Same as qsa_buffer_bytes (the sizing helper under its other name). */

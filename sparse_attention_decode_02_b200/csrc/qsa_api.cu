@@ -61,6 +61,68 @@ const char* config_problem(const qsa_config& c) {
 }
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+bool usable(const void* p, size_t a) { return p && aligned(p, a); }
+
+qsa_status status_of(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
+
+bool current_sms(int* n_sms) {
+  int dev = 0;
+  return cudaGetDevice(&dev) == cudaSuccess &&
+         cudaDeviceGetAttribute(n_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+}
+
+// Shape of a paged cache (the first five fields).
+qsa_status paged_shape(const qsa_paged_kv* c) {
+  if (!c) return QSA_ERR_INVALID_ARG;
+  if (c->n_pages < 1 || c->n_kv_heads < 1) return QSA_ERR_INVALID_ARG;
+  if (c->page_size < 16 || c->page_size > 256 || (c->page_size & (c->page_size - 1))) return QSA_ERR_UNSUPPORTED;
+  if (c->head_dim != 64 && c->head_dim != 128) return QSA_ERR_UNSUPPORTED;
+  if (c->n_kv_heads > 1024) return QSA_ERR_UNSUPPORTED;
+  if (c->format != QSA_PAGE_F16 && c->format != QSA_PAGE_FP8 && c->format != QSA_PAGE_INT4) return QSA_ERR_UNSUPPORTED;
+  return QSA_OK;
+}
+
+int64_t tight_page(const qsa_paged_kv& c) {
+  return int64_t(c.n_kv_heads) * c.page_size * page_row_bytes(c.format, c.head_dim);
+}
+int64_t tight_scales(const qsa_paged_kv& c) {
+  return int64_t(c.n_kv_heads) * c.page_size * page_scale_bytes(c.format, c.head_dim);
+}
+
+// The whole descriptor: shape, strides and buffers.
+qsa_status paged_view(const qsa_paged_kv* c, PagedView* v) {
+  if (qsa_status st = paged_shape(c)) return st;
+  const int64_t page = tight_page(*c), scales = tight_scales(*c);
+  v->page_stride = c->page_stride ? c->page_stride : page;
+  v->scale_stride = c->scale_stride ? c->scale_stride : scales;
+  if (v->page_stride < page || v->page_stride % 16 || v->scale_stride < scales || v->scale_stride % 16)
+    return QSA_ERR_INVALID_ARG;
+  if (!usable(c->k_pages, 16) || !usable(c->v_pages, 16)) return QSA_ERR_INVALID_ARG;
+  if (scales && (!usable(c->k_scales, 16) || !usable(c->v_scales, 16))) return QSA_ERR_INVALID_ARG;
+  v->k = static_cast<char*>(c->k_pages);
+  v->v = static_cast<char*>(c->v_pages);
+  v->ks = static_cast<char*>(c->k_scales);
+  v->vs = static_cast<char*>(c->v_scales);
+  v->n_pages = c->n_pages;
+  v->page_shift = __builtin_ctz(unsigned(c->page_size));
+  v->n_kv_heads = c->n_kv_heads;
+  v->head_dim = c->head_dim;
+  return QSA_OK;
+}
+
+// Checks the arguments qsa_paged_write and qsa_paged_read share. *empty: nothing to do.
+qsa_status paged_rows(const qsa_paged_kv& c, PagedRows* r, bool* empty) {
+  const int64_t row = int64_t(c.n_kv_heads) * c.head_dim;
+  if (r->n_rows < 0 || r->n_seqs < 0 || r->table_width < 0) return QSA_ERR_INVALID_ARG;
+  if (r->row_stride == 0) r->row_stride = row;
+  if (r->row_stride < row || r->row_stride % 8) return QSA_ERR_INVALID_ARG;
+  *empty = r->n_rows == 0 || r->n_seqs == 0;
+  if (*empty) return QSA_OK;
+  if (r->table_width < 1 || !usable(r->block_table, 4) || !usable(r->first, 4) || !usable(r->row_start, 4) ||
+      !aligned(r->status, 4))
+    return QSA_ERR_INVALID_ARG;
+  return QSA_OK;
+}
 
 }  // namespace
 
@@ -492,6 +554,120 @@ qsa_status qsa_rollback(qsa_ctx* ctx, int32_t layer, int32_t n_keep, qsa_stream_
   // and the pooled count is cut to them, so the count of blocks waiting to be pooled can
   // only fall (pending_blocks stays an upper bound).
   return ctx->cuda(launch_set_state(ctx->view(layer), n_keep, 0, kSetRollback, (cudaStream_t)stream), "rollback");
+}
+
+qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, const int32_t* n_accepted,
+                                 qsa_stream_t stream) {
+  if (!ctx) return QSA_ERR_INVALID_ARG;
+  if (qsa_status st = ctx->layer_ok(layer)) return st;
+  if (n_drafts < 0) return ctx->fail(QSA_ERR_INVALID_ARG, "n_drafts must be >= 0");
+  QSA_CHECK_PTR(n_accepted, 4, "n_accepted");
+  // like qsa_rollback, this only drops tokens: pending_blocks stays an upper bound
+  return ctx->cuda(launch_rollback_rejected(ctx->view(layer), n_drafts, n_accepted, (cudaStream_t)stream),
+                   "rollback_rejected");
+}
+
+qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs,
+                             int64_t draft_stride, const int32_t* draft_tokens, const int32_t* n_drafts,
+                             const float* uniforms, int32_t n_seqs, int32_t max_drafts, int32_t vocab,
+                             int32_t* n_accepted, int32_t* next_token, int32_t* status, qsa_stream_t stream) {
+  if (n_seqs < 0 || max_drafts < 0 || vocab < 1) return QSA_ERR_INVALID_ARG;
+  if (max_drafts > QSA_MAX_DRAFTS) return QSA_ERR_UNSUPPORTED;
+  if (target_stride == 0) target_stride = vocab;
+  if (draft_stride == 0) draft_stride = vocab;
+  if (target_stride < vocab || draft_stride < vocab) return QSA_ERR_INVALID_ARG;
+  if (n_seqs == 0) return QSA_OK;
+  if (!usable(target_probs, 4) || !aligned(draft_probs, 4) || !usable(uniforms, 4) || !usable(n_accepted, 4) ||
+      !usable(next_token, 4) || !aligned(n_drafts, 4) || !aligned(status, 4) ||
+      (max_drafts > 0 && !usable(draft_tokens, 4)))
+    return QSA_ERR_INVALID_ARG;
+  int n_sms = 0;
+  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  const VerifyArgs a{target_probs, target_stride, draft_probs, draft_stride, draft_tokens, n_drafts, uniforms,
+                     n_seqs,       max_drafts,    vocab,       n_accepted,   next_token,   status};
+  return status_of(launch_verify(a, n_sms, (cudaStream_t)stream));
+}
+
+size_t qsa_paged_bytes(const qsa_paged_kv* cache, int32_t which) {
+  if (paged_shape(cache) != QSA_OK) return 0;
+  switch (which) {
+    case QSA_PAGED_BUF_PAGES: return size_t(cache->n_pages) * size_t(tight_page(*cache));
+    case QSA_PAGED_BUF_SCALES: return size_t(cache->n_pages) * size_t(tight_scales(*cache));
+    default: return 0;
+  }
+}
+
+qsa_status qsa_paged_write(const qsa_paged_kv* cache, const void* k, const void* v, int64_t row_stride,
+                           int32_t n_rows, const int32_t* block_table, int32_t table_width, int32_t n_seqs,
+                           const int32_t* first, const int32_t* row_start, int32_t* status, qsa_stream_t stream) {
+  PagedView c;
+  if (qsa_status st = paged_view(cache, &c)) return st;
+  PagedRows r{block_table, table_width, n_seqs, first, row_start, n_rows, row_stride, status};
+  bool empty = false;
+  if (qsa_status st = paged_rows(*cache, &r, &empty)) return st;
+  if (empty) return QSA_OK;
+  if (!usable(k, 16) || !usable(v, 16)) return QSA_ERR_INVALID_ARG;
+  int n_sms = 0;
+  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  return status_of(launch_paged_write(c, cache->format, r, k, v, n_sms, (cudaStream_t)stream));
+}
+
+qsa_status qsa_paged_read(const qsa_paged_kv* cache, void* k, void* v, int64_t row_stride, int32_t n_rows,
+                          const int32_t* block_table, int32_t table_width, int32_t n_seqs, const int32_t* first,
+                          const int32_t* row_start, int32_t* status, qsa_stream_t stream) {
+  PagedView c;
+  if (qsa_status st = paged_view(cache, &c)) return st;
+  PagedRows r{block_table, table_width, n_seqs, first, row_start, n_rows, row_stride, status};
+  bool empty = false;
+  if (qsa_status st = paged_rows(*cache, &r, &empty)) return st;
+  if (empty || (!k && !v)) return QSA_OK;
+  if (!aligned(k, 16) || !aligned(v, 16)) return QSA_ERR_INVALID_ARG;
+  int n_sms = 0;
+  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  return status_of(launch_paged_read(c, cache->format, r, k, v, n_sms, (cudaStream_t)stream));
+}
+
+static qsa_status paged_heads(const qsa_paged_kv& c, int32_t n_q_heads, int32_t n_queries) {
+  if (n_q_heads < 1 || n_queries < 1) return QSA_ERR_INVALID_ARG;
+  if (n_q_heads % c.n_kv_heads || n_q_heads / c.n_kv_heads > 8 || n_queries > QSA_MAX_QUERIES)
+    return QSA_ERR_UNSUPPORTED;
+  return QSA_OK;
+}
+
+size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, int32_t n_queries) {
+  if (paged_shape(cache) != QSA_OK || paged_heads(*cache, n_q_heads, n_queries) != QSA_OK) return 0;
+  int n_sms = 0;
+  if (!current_sms(&n_sms)) {
+    cudaGetLastError();
+    n_sms = 148;
+  }
+  return paged_workspace_bytes(cache->head_dim, n_q_heads, cache->n_kv_heads, n_queries, n_sms);
+}
+
+qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_stride, int32_t n_queries,
+                            int32_t n_q_heads, const int32_t* block_table, int32_t table_width, int32_t n_seqs,
+                            const int32_t* seq_lens, float sm_scale, float* out, float* lse, void* workspace,
+                            size_t workspace_bytes, int32_t* status, qsa_stream_t stream) {
+  PagedView c;
+  if (qsa_status st = paged_view(cache, &c)) return st;
+  if (qsa_status st = paged_heads(*cache, n_q_heads, n_queries)) return st;
+  const int64_t row = int64_t(n_q_heads) * cache->head_dim;
+  if (q_stride == 0) q_stride = row;
+  if (q_stride < row || q_stride % 8 || n_seqs < 0 || table_width < 0) return QSA_ERR_INVALID_ARG;
+  if (!(sm_scale >= 0.0f) || sm_scale > 1e30f) return QSA_ERR_INVALID_ARG;
+  if (n_seqs == 0) return QSA_OK;
+  if (n_seqs > 65536) return QSA_ERR_UNSUPPORTED;
+  if (table_width < 1 || !usable(q, 16) || !usable(block_table, 4) || !usable(seq_lens, 4) || !usable(out, 16) ||
+      !aligned(lse, 4) || !usable(workspace, 256) || !aligned(status, 4))
+    return QSA_ERR_INVALID_ARG;
+  int n_sms = 0;
+  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  if (workspace_bytes < paged_workspace_bytes(cache->head_dim, n_q_heads, cache->n_kv_heads, n_queries, n_sms))
+    return QSA_ERR_CAPACITY;
+  if (sm_scale == 0.0f) sm_scale = cache->head_dim == 64 ? 0.125f : 0.088388347648318447f;
+  const PagedAttendArgs a{q,        q_stride, n_queries, n_q_heads, block_table, table_width, n_seqs,
+                          seq_lens, sm_scale, out,       lse,       workspace,   status};
+  return status_of(launch_paged_attend(c, cache->format, a, n_sms, (cudaStream_t)stream));
 }
 
 qsa_status qsa_cp_index_candidates(qsa_ctx* ctx, int32_t layer, const void* q_idx, const float* w, int32_t n_global,

@@ -49,6 +49,24 @@ cudaError_t launch_set_state(const LayerView& L, int n_ctx, int n_pooled, int mo
   return launch_pdl(set_state_kernel, dim3(1), dim3(32), 0, s, 1, L.state, n_ctx, n_pooled, mode);
 }
 
+__global__ void rollback_rejected_kernel(DevState* st, int n_drafts, const int32_t* __restrict__ n_accepted) {
+  pdl_launch_dependents();
+  pdl_wait();
+  if (threadIdx.x != 0) return;
+  int m = *n_accepted;
+  if (m < 0 || m > n_drafts) {
+    record_status(st, QSA_ERR_BAD_INDEX);
+    m = m < 0 ? 0 : n_drafts;
+  }
+  const int n = st->n_ctx, keep = max(n - (n_drafts - m), 0);
+  st->n_ctx = keep;
+  if (st->n_pooled > keep / kBlock) st->n_pooled = keep / kBlock;
+}
+
+cudaError_t launch_rollback_rejected(const LayerView& L, int n_drafts, const int32_t* n_accepted, cudaStream_t s) {
+  return launch_pdl(rollback_rejected_kernel, dim3(1), dim3(32), 0, s, 1, L.state, n_drafts, n_accepted);
+}
+
 // Appends n tokens at position n_ctx: three contiguous copies (token-major caches), in
 // 16-byte units (FP8: the K/V rows quantised a warp per row). All CTAs read n_ctx before
 // any of them can change it: the last CTA to finish (atomic ticket) publishes n_ctx + n.

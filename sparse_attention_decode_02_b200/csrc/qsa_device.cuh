@@ -53,6 +53,11 @@ __device__ __forceinline__ void record_status(DevState* st, int code) {
   atomicCAS(&st->status, 0, code);
 }
 
+// The status word of a call without a layer (may be null).
+__device__ __forceinline__ void record_status(int32_t* status, int code) {
+  if (status) atomicCAS(status, 0, code);
+}
+
 __device__ __forceinline__ int ld_volatile(const int32_t* p) { return *(volatile const int32_t*)p; }
 
 // Sum over the 32 lanes in a fixed butterfly order (deterministic).

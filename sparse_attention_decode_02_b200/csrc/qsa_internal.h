@@ -173,6 +173,72 @@ cudaError_t launch_attend_split(const LayerView& L, const void* q, const int32_t
                                 const int32_t* n_cells, float* out, cudaStream_t s);
 cudaError_t plan_attention(const qsa_config& c, int* cluster, int* cells_per_cta);
 
+// Of the n_drafts newest tokens keep the first *n_accepted (device count).
+cudaError_t launch_rollback_rejected(const LayerView& L, int n_drafts, const int32_t* n_accepted, cudaStream_t s);
+
+// ---- paged K/V cache (qsa_paged.cu, qsa_paged_attend.cu) ----
+// A qsa_paged_kv as the kernels take it: strides filled in, page_size as a shift.
+struct PagedView {
+  char *k, *v, *ks, *vs;
+  int64_t page_stride, scale_stride;
+  int n_pages, page_shift, n_kv_heads, head_dim;
+};
+
+inline int page_row_bytes(int format, int head_dim) {
+  return format == QSA_PAGE_F16 ? 2 * head_dim : format == QSA_PAGE_FP8 ? head_dim : head_dim / 2;
+}
+inline int page_scale_bytes(int format, int head_dim) {  // of one row
+  return format == QSA_PAGE_F16 ? 0 : format == QSA_PAGE_FP8 ? 4 : head_dim / 32 * 2;
+}
+
+// Which rows of a write or a read go where: sequence s has rows [row_start[s], row_start[s + 1])
+// at positions first[s] on, in the pages its block-table row lists.
+struct PagedRows {
+  const int32_t* block_table;
+  int table_width, n_seqs;
+  const int32_t* first;
+  const int32_t* row_start;
+  int n_rows;
+  int64_t row_stride;  // elements
+  int32_t* status;
+};
+cudaError_t launch_paged_write(const PagedView& c, int format, const PagedRows& r, const void* k, const void* v,
+                               int n_sms, cudaStream_t s);
+cudaError_t launch_paged_read(const PagedView& c, int format, const PagedRows& r, void* k, void* v, int n_sms,
+                              cudaStream_t s);
+
+struct PagedAttendArgs {
+  const void* q;
+  int64_t q_stride;  // elements
+  int n_queries, n_q_heads;
+  const int32_t* block_table;
+  int table_width, n_seqs;
+  const int32_t* seq_lens;
+  float sm_scale;
+  float* out;
+  float* lse;
+  void* workspace;
+  int32_t* status;
+};
+size_t paged_workspace_bytes(int head_dim, int n_q_heads, int n_kv_heads, int n_queries, int n_sms);
+cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, cudaStream_t s);
+
+// ---- draft verification (qsa_verify.cu) ----
+struct VerifyArgs {
+  const float* target;
+  int64_t target_stride;
+  const float* draft;
+  int64_t draft_stride;
+  const int32_t* tokens;
+  const int32_t* n_drafts;
+  const float* uniforms;
+  int n_seqs, max_drafts, vocab;
+  int32_t* n_accepted;
+  int32_t* next_token;
+  int32_t* status;
+};
+cudaError_t launch_verify(const VerifyArgs& a, int n_sms, cudaStream_t s);
+
 // set_state modes
 enum { kSetReset = 0, kSetRestore = 1, kSetInvalidate = 2, kSetClearStatus = 3, kSetRollback = 4 };
 

@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import c_float, c_int32, c_size_t, c_void_p
+from ctypes import c_float, c_int32, c_int64, c_size_t, c_void_p
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libqsa.so")
@@ -25,6 +25,9 @@ QSA_SCAN_TENSOR, QSA_SCAN_CUDA_CORES = 0, 1
 QSA_POOLED_F16, QSA_POOLED_FP8 = 0, 1
 QSA_INPUTS_ORDERED, QSA_INPUTS_EARLY = 0, 1
 QSA_MAX_QUERIES = 4
+QSA_MAX_DRAFTS = 64
+QSA_PAGE_F16, QSA_PAGE_FP8, QSA_PAGE_INT4 = range(3)
+QSA_PAGED_BUF_PAGES, QSA_PAGED_BUF_SCALES = 0, 1
 
 
 class QsaError(RuntimeError):
@@ -48,8 +51,18 @@ class QsaLayerBuffers(ctypes.Structure):
                 ("kv_scales", c_void_p), ("pooled_scales", c_void_p)]
 
 
+class QsaPagedKv(ctypes.Structure):
+    _fields_ = [("n_pages", c_int32), ("page_size", c_int32), ("n_kv_heads", c_int32), ("head_dim", c_int32),
+                ("format", c_int32), ("reserved", c_int32), ("page_stride", c_int64), ("scale_stride", c_int64),
+                ("k_pages", c_void_p), ("v_pages", c_void_p), ("k_scales", c_void_p), ("v_scales", c_void_p)]
+
+
 _P = c_void_p
 _I = c_int32
+_L = c_int64
+_F = c_float
+_Z = c_size_t
+_KV = ctypes.POINTER(QsaPagedKv)
 # name -> (restype, argtypes); must list every function include/qsa.h declares
 SIGNATURES = {
     "qsa_buffer_bytes": (c_size_t, [ctypes.POINTER(QsaConfig), _I]),
@@ -82,6 +95,13 @@ SIGNATURES = {
     "qsa_cp_select": (_I, [_P, _P, _I, _I, _P, _P, _P]),
     "qsa_cp_attend_partial": (_I, [_P, _I, _P, _P, _P, _I, _P, _P, _P]),
     "qsa_cp_merge": (_I, [_P, _P, _I, _I, _I, _P, _P]),
+    "qsa_rollback_rejected": (_I, [_P, _I, _I, _P, _P]),
+    "qsa_verify_drafts": (_I, [_P, _L, _P, _L, _P, _P, _P, _I, _I, _I, _P, _P, _P, _P]),
+    "qsa_paged_bytes": (c_size_t, [_KV, _I]),
+    "qsa_paged_write": (_I, [_KV, _P, _P, _L, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "qsa_paged_read": (_I, [_KV, _P, _P, _L, _I, _P, _I, _I, _P, _P, _P, _P]),
+    "qsa_paged_workspace_bytes": (c_size_t, [_KV, _I, _I]),
+    "qsa_paged_attend": (_I, [_KV, _P, _L, _I, _I, _P, _I, _I, _P, _F, _P, _P, _P, _Z, _P, _P]),
 }
 
 _lib = None
@@ -238,6 +258,11 @@ class Qsa:
     def rollback(self, layer, n_keep, stream=None):
         self._check(self.lib.qsa_rollback(self.handle, layer, int(n_keep), _stream(stream)))
 
+    def rollback_rejected(self, layer, n_drafts, n_accepted, stream=None):
+        """Of the n_drafts newest tokens keep the first n_accepted (a device i32)."""
+        self._check(self.lib.qsa_rollback_rejected(self.handle, layer, int(n_drafts), _ptr(n_accepted),
+                                                   _stream(stream)))
+
     def decode_step(self, layer, k, v, idx_key, q_idx, w, q, sel_blocks, n_sel, out, stream=None):
         """The whole hot path of one decode step of one layer in one ABI call."""
         self._check(self.lib.qsa_decode_step(self.handle, layer, _ptr(k), _ptr(v), _ptr(idx_key), _ptr(q_idx),
@@ -297,6 +322,203 @@ def sparse_attend_noalloc(q, k_cache, v_cache, n_ctx, cells, n_cells, out, n_q_h
                                                   top_k_tokens, _stream(stream))
     if st != QSA_OK:
         raise QsaError(st, "qsa_sparse_attend_noalloc failed")
+
+
+def _here(*tensors):
+    """Checks that every tensor lives on the current device, where a call without a context runs."""
+    import torch
+    at = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and t.get_device() != at:
+            raise ValueError(f"tensors must live on the current device cuda:{at} (one is on {t.device})")
+
+
+def _want(name, t, dtype, shape):
+    """Checks the type and shape of an argument (None in `shape`: any size)."""
+    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
+        want = " x ".join("?" if w is None else str(w) for w in shape)
+        raise ValueError(f"{name} must be {dtype} of shape [{want}], got {t.dtype} {tuple(t.shape)}")
+
+
+class PagedKV:
+    """A paged K/V cache over tensors the caller owns (qsa_paged_kv):
+    k_pages, v_pages [n_pages, n_kv_heads, page_size, row] with rows of head_dim f16 values
+    (QSA_PAGE_F16), head_dim e4m3 codes (QSA_PAGE_FP8, a one-byte type) or head_dim/2 bytes of
+    4-bit codes (QSA_PAGE_INT4); k_scales, v_scales [n_pages, n_kv_heads, page_size] f32
+    (FP8) or [n_pages, n_kv_heads, page_size, head_dim/32] f16 (INT4). Pages may lie apart
+    (a layer's part of one pool: stride(0) larger than a page), the rest is contiguous."""
+
+    def __init__(self, k_pages, v_pages, page_format, k_scales=None, v_scales=None):
+        import torch
+        self.lib = load_library()
+        self.tensors = (k_pages, v_pages, k_scales, v_scales)  # kept alive with the descriptor
+        if page_format not in (QSA_PAGE_F16, QSA_PAGE_FP8, QSA_PAGE_INT4):
+            raise ValueError("page_format must be QSA_PAGE_F16, QSA_PAGE_FP8 or QSA_PAGE_INT4")
+        if k_pages.dim() != 4:
+            raise ValueError("k_pages must be [n_pages, n_kv_heads, page_size, row]")
+        n, heads, page, row = k_pages.shape
+        self.head_dim = 2 * row if page_format == QSA_PAGE_INT4 else row
+        self.n_kv_heads, self.device = heads, k_pages.get_device()
+        types = (torch.float16,) if page_format == QSA_PAGE_F16 else (torch.uint8, torch.float8_e4m3fn)
+        if page_format == QSA_PAGE_INT4:
+            types = (torch.uint8,)
+        if k_pages.dtype not in types:
+            raise ValueError(f"k_pages must be one of {types}")
+        _want("v_pages", v_pages, k_pages.dtype, (n, heads, page, row))
+        if page_format != QSA_PAGE_F16:
+            if k_scales is None or v_scales is None:
+                raise ValueError("this page format has scales")
+            shape = (n, heads, page) if page_format == QSA_PAGE_FP8 else (n, heads, page, self.head_dim // 32)
+            kind = torch.float32 if page_format == QSA_PAGE_FP8 else torch.float16
+            _want("k_scales", k_scales, kind, shape)
+            _want("v_scales", v_scales, kind, shape)
+        else:
+            k_scales = v_scales = None
+
+        def stride(a, b):  # bytes between pages; pages themselves contiguous
+            if a is None:
+                return 0
+            for t in (a, b):
+                if not t.is_cuda or t.get_device() != self.device:
+                    raise ValueError("pages and scales must live on one GPU")
+                if not t[0].is_contiguous() or (n > 1 and (t.stride(0) != a.stride(0) or t.stride(0) < t[0].numel())):
+                    raise ValueError("pages must be contiguous and K and V pages equally far apart")
+            return a.stride(0) * a.element_size() if n > 1 else 0
+
+        addr = [None if t is None else t.data_ptr() for t in (k_pages, v_pages, k_scales, v_scales)]
+        self.desc = QsaPagedKv(n, page, heads, self.head_dim, page_format, 0, stride(k_pages, v_pages),
+                               stride(k_scales, v_scales), *addr)
+        self._ref = ctypes.byref(self.desc)
+        if n < 1 or self.lib.qsa_paged_bytes(self._ref, QSA_PAGED_BUF_PAGES) == 0:
+            raise QsaError(5, "no such paged cache: page_size 16..256 (a power of two), head_dim 64 or 128")
+
+    def _rows(self, k, v, block_table, first, row_start, status):
+        import torch
+        a = k if k is not None else v
+        if a is None:
+            raise ValueError("k and v must not both be None")
+        for name, t in (("k", k), ("v", v)):
+            if t is not None:
+                _want(name, t, torch.float16, (a.shape[0], self.n_kv_heads, self.head_dim))
+                if t.numel() and (t.stride(2) != 1 or (self.n_kv_heads > 1 and t.stride(1) != self.head_dim) or
+                                  (t.shape[0] > 1 and (t.stride(0) != a.stride(0) or t.stride(0) < t[0].numel()))):
+                    raise ValueError("rows must be contiguous and those of k and v equally far apart")
+        n_seqs = block_table.shape[0]
+        _want("block_table", block_table, torch.int32, (n_seqs, None))
+        _want("first", first, torch.int32, (n_seqs,))
+        _want("row_start", row_start, torch.int32, (n_seqs + 1,))
+        _here(k, v, block_table, first, row_start, status, self.tensors[0])
+        stride = a.stride(0) if a.shape[0] > 1 else 0
+        return (k.data_ptr() if k is not None else None, v.data_ptr() if v is not None else None, stride,
+                a.shape[0], _ptr(block_table), block_table.shape[1], n_seqs, _ptr(first), _ptr(row_start),
+                _status_ptr(status))
+
+    def write(self, k, v, block_table, first, row_start, status=None, stream=None):
+        """qsa_paged_write: stores rows k, v [n_rows, n_kv_heads, head_dim] f16 (rows may lie apart)."""
+        if k is None or v is None:
+            raise ValueError("k and v must be tensors")
+        args = self._rows(k, v, block_table, first, row_start, status)
+        st = self.lib.qsa_paged_write(self._ref, *args, _stream(stream))
+        if st != QSA_OK:
+            raise QsaError(st, "qsa_paged_write failed")
+
+    def read(self, k, v, block_table, first, row_start, status=None, stream=None):
+        """qsa_paged_read: rows back as f16 values, into k and v (either may be None)."""
+        args = self._rows(k, v, block_table, first, row_start, status)
+        st = self.lib.qsa_paged_read(self._ref, *args, _stream(stream))
+        if st != QSA_OK:
+            raise QsaError(st, "qsa_paged_read failed")
+
+    def workspace_bytes(self, n_q_heads, n_queries=1) -> int:
+        """Bytes of the workspace of attend() with these heads and queries."""
+        n = int(self.lib.qsa_paged_workspace_bytes(self._ref, n_q_heads, n_queries))
+        if n == 0:
+            raise QsaError(5, "n_q_heads / n_kv_heads must be 1..8 and n_queries 1..4")
+        return n
+
+    def attend(self, q, block_table, seq_lens, out, workspace, lse=None, sm_scale=0.0, status=None, stream=None):
+        """qsa_paged_attend: q [n_seqs, n_queries, n_q_heads, head_dim] f16 (query rows may lie
+        apart evenly), out the same f32, lse [n_seqs, n_queries, n_q_heads] f32."""
+        import torch
+        n_seqs, n_queries, n_q_heads = q.shape[:3]
+        _want("q", q, torch.float16, (n_seqs, n_queries, n_q_heads, self.head_dim))
+        _want("out", out, torch.float32, (n_seqs, n_queries, n_q_heads, self.head_dim))
+        _want("block_table", block_table, torch.int32, (n_seqs, None))
+        _want("seq_lens", seq_lens, torch.int32, (n_seqs,))
+        if lse is not None:
+            _want("lse", lse, torch.float32, (n_seqs, n_queries, n_q_heads))
+        _here(q, block_table, seq_lens, out, workspace, lse, status, self.tensors[0])
+        stride = 0
+        if q.numel():
+            stride = q.stride(1) if n_queries > 1 else q.stride(0) if n_seqs > 1 else 0
+            if (not q[0, 0].is_contiguous() or (n_seqs * n_queries > 1 and stride < q[0, 0].numel()) or
+                    (n_seqs > 1 and q.stride(0) != n_queries * stride)):
+                raise ValueError("query rows must be contiguous and equally far apart")
+        st = self.lib.qsa_paged_attend(self._ref, q.data_ptr(), stride, n_queries, n_q_heads, _ptr(block_table),
+                                       block_table.shape[1], n_seqs, _ptr(seq_lens), sm_scale, _ptr(out), _ptr(lse),
+                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
+                                       _status_ptr(status), _stream(stream))
+        if st != QSA_OK:
+            raise QsaError(st, "qsa_paged_attend failed")
+
+
+def _status_ptr(status):
+    if status is None:
+        return None
+    import torch
+    if status.dtype != torch.int32 or status.numel() < 1:
+        raise ValueError("status must be an int32 tensor")
+    return _ptr(status)
+
+
+def alloc_paged_kv(n_pages, page_size, n_kv_heads, head_dim, page_format=QSA_PAGE_F16, device="cuda") -> PagedKV:
+    """Allocates the buffers of a paged cache with torch (`.tensors`: k and v pages, k and v scales)."""
+    import torch
+    row, kind = {QSA_PAGE_F16: (head_dim, torch.float16), QSA_PAGE_FP8: (head_dim, torch.uint8),
+                 QSA_PAGE_INT4: (head_dim // 2, torch.uint8)}[page_format]
+    pages = [torch.zeros(n_pages, n_kv_heads, page_size, row, dtype=kind, device=device) for _ in range(2)]
+    scales = [None, None]
+    if page_format == QSA_PAGE_FP8:
+        scales = [torch.ones(n_pages, n_kv_heads, page_size, device=device) for _ in range(2)]
+    elif page_format == QSA_PAGE_INT4:
+        scales = [torch.zeros(n_pages, n_kv_heads, page_size, head_dim // 32, dtype=torch.float16, device=device)
+                  for _ in range(2)]
+    return PagedKV(*pages, page_format, *scales)
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, n_accepted, next_token, n_drafts=None, status=None,
+                  stream=None):
+    """qsa_verify_drafts: target_probs [n_seqs, max_drafts + 1, vocab] f32, draft_probs [n_seqs,
+    max_drafts, vocab] f32 or None (rows of both may lie apart evenly), draft_tokens [n_seqs,
+    max_drafts] i32, uniforms [n_seqs, max_drafts + 1] f32 -> n_accepted, next_token [n_seqs] i32."""
+    import torch
+    n_seqs, rows, vocab = target_probs.shape
+    k = rows - 1
+    _want("target_probs", target_probs, torch.float32, (n_seqs, rows, vocab))
+    _want("draft_tokens", draft_tokens, torch.int32, (n_seqs, k))
+    _want("uniforms", uniforms, torch.float32, (n_seqs, rows))
+    _want("n_accepted", n_accepted, torch.int32, (n_seqs,))
+    _want("next_token", next_token, torch.int32, (n_seqs,))
+    if n_drafts is not None:
+        _want("n_drafts", n_drafts, torch.int32, (n_seqs,))
+    strides = []
+    for name, t, r in (("target_probs", target_probs, rows), ("draft_probs", draft_probs, k)):
+        if t is None or t.numel() == 0:
+            strides.append(0)
+            continue
+        _want(name, t, torch.float32, (n_seqs, r, vocab))
+        s = t.stride(1) if r > 1 else t.stride(0) if n_seqs > 1 else 0
+        if (not t[0, 0].is_contiguous() or (n_seqs * r > 1 and s < vocab) or
+                (n_seqs > 1 and t.stride(0) != r * s)):
+            raise ValueError(f"rows of {name} must be contiguous and equally far apart")
+        strides.append(s)
+    _here(target_probs, draft_probs, draft_tokens, uniforms, n_accepted, next_token, n_drafts, status)
+    st = load_library().qsa_verify_drafts(
+        target_probs.data_ptr(), strides[0], None if draft_probs is None else draft_probs.data_ptr(), strides[1],
+        _ptr(draft_tokens), _ptr(n_drafts), _ptr(uniforms), n_seqs, k, vocab, _ptr(n_accepted), _ptr(next_token),
+        _status_ptr(status), _stream(stream))
+    if st != QSA_OK:
+        raise QsaError(st, "qsa_verify_drafts failed")
 
 
 def alloc_layer(cfg: QsaConfig, device="cuda"):

@@ -1,0 +1,577 @@
+"""The paged K/V cache on the GPU against plain float64 forms: quantised writes, reads back,
+attention of the newest tokens, and the calls together as a serving loop makes them.
+
+Codes, scales and values read back must be exact. The attention's tolerance is derived: a
+logit is an f32 sum of D exact products, off by at most D f32 units (2^-23, a truncating
+sum) of sum|q k|, and its exponential by two units more; that error e enters numerator
+and denominator; the sums over n cells add at most n units, the rest of the chain (scale,
+split f16 weights, merge) a few tens of units. A weight is held as two f16 terms of
+2^15 p, p <= 1 relative to the largest: what is below half an f16 subnormal step of them,
+2^-25 2^-15, is lost, so each of the n weights is off by 2^-40 at most (this term counts
+where an output's own weights are all tiny).
+"""
+import numpy as np
+import pytest
+import torch
+
+import sparse_attention_decode_02_b200 as Q
+from oracle import paged_oracle as P
+from tests import gpu_harness as H
+
+pytestmark = pytest.mark.gpu
+
+FORMATS = {"f16": Q.QSA_PAGE_F16, "fp8": Q.QSA_PAGE_FP8, "int4": Q.QSA_PAGE_INT4}
+BAD_INDEX, CAPACITY = 6, 2
+UNIT = 2.0 ** -23
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    H.ensure_library()
+
+
+def _i32(a):
+    return torch.as_tensor(np.asarray(a, np.int32), device="cuda")
+
+
+class Pool:
+    """A paged cache of sequences with the given capacities, its pages in random order, and
+    the f16 rows written to it (one array a sequence)."""
+
+    def __init__(self, caps, fmt, heads, dim, page, seed=0, spare=3, gap=0, poison=True):
+        self.rng = np.random.default_rng(seed)
+        self.fmt, self.heads, self.dim, self.page = fmt, heads, dim, page
+        need = [-(-c // page) for c in caps]
+        self.width, n = max(max(need), 1), sum(need) + spare
+        row, kind = {"f16": (dim, torch.float16), "fp8": (dim, torch.uint8), "int4": (dim // 2, torch.uint8)}[fmt]
+        mk = lambda *s, dtype: torch.zeros(n, 1 + gap, *s, dtype=dtype, device="cuda")  # noqa: E731
+        self.big = [mk(heads, page, row, dtype=kind) for _ in range(2)]
+        if fmt != "f16":
+            s = (heads, page) if fmt == "fp8" else (heads, page, dim // 32)
+            self.big += [mk(*s, dtype=torch.float32 if fmt == "fp8" else torch.float16) for _ in range(2)]
+        if poison:     # what no sequence holds is NaN
+            for t in self.big:
+                t.fill_(float("nan") if t.dtype != torch.uint8 else 0x7F)
+        parts = [t[:, gap] for t in self.big]     # with a gap: one layer of a pool of several
+        self.cache = Q.PagedKV(parts[0], parts[1], FORMATS[fmt], *parts[2:])
+        self.parts = parts + [None] * (4 - len(parts))
+        ids = self.rng.permutation(n)
+        self.table = np.full((len(caps), self.width), -1, np.int64)   # unused entries are no page
+        at = 0
+        for i, k in enumerate(need):
+            self.table[i, :k] = ids[at:at + k]
+            at += k
+        self.table_dev = _i32(self.table)
+        self.lens = [0] * len(caps)
+        self.rows = [[np.zeros((0, heads, dim), np.float16) for _ in caps] for _ in range(2)]
+        self.status = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def random_rows(self, counts, scale=1.0):
+        n = sum(counts)
+        return [(self.rng.standard_normal((n, self.heads, self.dim)) * scale).astype(np.float16) for _ in range(2)]
+
+    def append(self, counts, kv=None, stream=None):
+        k, v = kv if kv is not None else self.random_rows(counts)
+        start = np.concatenate([[0], np.cumsum(counts)])
+        self.cache.write(H.to_dev(k), H.to_dev(v), self.table_dev, _i32(self.lens), _i32(start), status=self.status,
+                         stream=stream)
+        for i, c in enumerate(counts):
+            for x, rows in ((k, self.rows[0]), (v, self.rows[1])):
+                rows[i] = np.concatenate([rows[i][:self.lens[i]], x[start[i]:start[i + 1]]])
+            self.lens[i] += c
+        return k, v
+
+    def values(self, i):
+        """The float64 K and V of sequence i that its stored rows stand for."""
+        return [P.values(*P.quantise(rows[i], self.fmt), self.fmt) for rows in self.rows]
+
+    def attend(self, q, lse=True, sm_scale=0.0, lens=None, **kw):
+        S, T, Hq, D = q.shape
+        out = torch.full((S, T, Hq, D), float("nan"), device="cuda")
+        l = torch.full((S, T, Hq), float("nan"), device="cuda") if lse else None
+        ws = torch.full((self.cache.workspace_bytes(Hq, T),), 0xFF, dtype=torch.uint8, device="cuda")
+        self.cache.attend(q if torch.is_tensor(q) else H.to_dev(q), self.table_dev,
+                          _i32(self.lens if lens is None else lens), out, ws, lse=l, sm_scale=sm_scale,
+                          status=self.status, **kw)
+        return out, l
+
+    def check(self, q, out, lse, sm_scale=None, code=0):
+        out = out.cpu().numpy().astype(np.float64)
+        lse = lse.cpu().numpy().astype(np.float64)
+        for i, n in enumerate(self.lens):
+            k, v = self.values(i)
+            assert_attention(out[i], lse[i], q[i], k, v, sm_scale, f"sequence {i} of {n} tokens")
+        assert int(self.status) == code
+
+
+def assert_attention(out, lse, q, k, v, sm_scale=None, what=""):
+    want, want_lse, bound, depth = P.attention(q, k, v, sm_scale)
+    n, D = len(k), q.shape[-1]
+    e = (D * depth + 8 * (np.abs(np.where(np.isfinite(want_lse), want_lse, 0)) + depth + 1)) * UNIT
+    tol = (2 * e[..., None] + (n + 64) * UNIT) * bound + n * 2.0 ** -40 * np.abs(v).max(initial=0.0)
+    assert np.isfinite(out).all(), f"{what}: out is not finite"
+    assert (np.abs(out - want) <= tol).all(), f"{what}: {np.max(np.abs(out - want) / np.maximum(tol, 1e-30)):.3g} of tolerance"
+    empty = np.isinf(want_lse)
+    assert np.array_equal(np.isneginf(lse), empty), what
+    tol = e + (n + 64) * UNIT
+    assert (np.abs(lse - np.where(empty, 0, want_lse))[~empty] <= tol[~empty]).all(), f"{what}: lse"
+
+
+def _query(rng, S, T, Hq, D, scale=1.0):
+    return (rng.standard_normal((S, T, Hq, D)) * scale).astype(np.float16)
+
+
+# ------------------------------------------------------------------ write and read
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads,dim,page,gap", [(1, 64, 16, 0), (4, 128, 32, 0), (3, 64, 128, 2), (8, 128, 256, 1)])
+def test_written_rows_are_exact_and_nothing_else_changes(fmt, heads, dim, page, gap):
+    counts = [5, 0, 1, 40, 0, 300, 17]
+    p = Pool([60, 4, 30, 100, 0, 310, 40], fmt, heads, dim, page, seed=dim + page, gap=gap)
+    p.lens = [11, 0, 29, 3, 0, 10, 16]     # what they hold already is not looked at here
+    for i, n in enumerate(p.lens):
+        for rows in p.rows:
+            rows[i] = np.zeros((n, heads, dim), np.float16)
+    old, before = [t.clone() for t in p.big], list(p.lens)
+    k, v = p.append(counts)
+    torch.cuda.synchronize()
+    assert int(p.status) == 0
+    want = [t.cpu().numpy().copy() for t in old]
+    at = 0
+    for i, c in enumerate(counts):
+        for j in range(c):
+            pos = before[i] + j
+            for t, x in ((0, k), (1, v)):
+                codes, scales = P.quantise(x[at], fmt)
+                want[t][p.table[i, pos // page], gap, :, pos % page] = codes
+                if scales is not None:
+                    want[t + 2][p.table[i, pos // page], gap, :, pos % page] = scales
+            at += 1
+    for t, w in zip(p.big, want):
+        got = t.cpu().numpy()
+        assert np.array_equal(got.view(np.uint8), w.view(np.uint8))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("heads,dim,page", [(1, 64, 16), (4, 128, 64), (5, 128, 16)])
+def test_rows_read_back_are_the_stored_values(fmt, heads, dim, page):
+    p = Pool([200, 3, 0, 77], fmt, heads, dim, page, seed=1)
+    p.append([190, 1, 0, 77])
+    first, counts = [13, 0, 0, 70], [150, 1, 0, 7]
+    start = np.concatenate([[0], np.cumsum(counts)])
+    n = start[-1]
+    full = lambda: torch.full((n + 5, heads, dim), 9.0, dtype=torch.float16, device="cuda")  # noqa: E731
+    k, v, only = full(), full(), full()
+    p.cache.read(k, v, p.table_dev, _i32(first), _i32(start), status=p.status)
+    p.cache.read(None, only, p.table_dev, _i32(first), _i32(start), status=p.status)
+    assert int(p.status) == 0
+    for t, got in ((0, k), (1, v), (1, only)):
+        want = np.full((n + 5, heads, dim), 9.0, np.float16)    # rows behind the last sequence stay
+        for i, c in enumerate(counts):
+            codes, scales = P.quantise(p.rows[t][i][first[i]:first[i] + c], fmt)
+            if fmt == "fp8":    # the f32 product, rounded to f16
+                x = P.values(codes, np.ones_like(scales), fmt).astype(np.float32) * scales[..., None]
+            else:
+                x = P.values(codes, scales, fmt)
+            want[start[i]:start[i + 1]] = x.astype(np.float16)
+        assert np.array_equal(got.cpu().numpy(), want)
+
+
+def test_rows_of_a_fused_projection_and_special_values():
+    """Rows that lie apart, and zeros, tiny, huge, infinite and NaN values."""
+    for fmt in FORMATS:
+        p = Pool([64], fmt, 2, 128, 16)
+        fused = torch.randn(40, 1024, device="cuda").half()
+        rows = fused.cpu().numpy()
+        k, v = fused[:, 512:768].unflatten(1, (2, 128)), fused[:, 768:].unflatten(1, (2, 128))
+        fused[3, 512:640] = 0
+        fused[4, 512:520] = 6e-8
+        fused[5, 512:640] *= 2e4
+        fused[6, 520] = float("inf")
+        fused[7, 600] = float("nan")
+        fused[8, 512:640] = 6e-8
+        rows = fused.cpu().numpy()
+        start, first = _i32([0, 40]), _i32([0])
+        p.cache.write(k, v, p.table_dev, first, start, status=p.status)
+        back = torch.empty(40, 1024, dtype=torch.float16, device="cuda")
+        p.cache.read(back[:, :256].unflatten(1, (2, 128)), back[:, 256:512].unflatten(1, (2, 128)), p.table_dev, first,
+                     start, status=p.status)
+        got = back[:, :512].reshape(40, 4, 128).cpu().numpy()
+        src = rows[:, 512:].reshape(40, 4, 128)
+        fine = [r for r in range(40) if r not in (6, 7)]
+        codes, scales = P.quantise(src[fine], fmt)
+        want = P.values(codes, np.ones_like(scales), fmt).astype(np.float32) * scales[..., None] if fmt == "fp8" \
+            else P.values(codes, scales, fmt)
+        assert np.array_equal(got[fine], want.astype(np.float16)), fmt
+        if fmt == "f16":
+            assert np.array_equal(got.view(np.uint16), src.view(np.uint16))
+        else:       # not finite where the input is not, the other heads' rows untouched by it
+            assert not np.isfinite(got[6, 0, 8]) and np.isnan(got[7, 0, 88])
+            assert np.isfinite(got[6:8, 1:]).all()
+            if fmt == "int4":
+                assert np.isnan(got[6, 0, :32]).all() and np.isfinite(got[6, 0, 32:]).all()
+                assert np.isnan(got[7, 0, 64:96]).all() and np.isfinite(got[7, 0, :64]).all()
+        assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_rows_without_a_place_are_skipped_and_reported(fmt):
+    p = Pool([32, 32, 32], fmt, 2, 64, 16)
+    p.append([32, 32, 32])
+    old = [t.clone() for t in p.big]
+    k = torch.randn(4, 2, 64, device="cuda").half()
+    cases = [([33, 0, 0], [0, 4, 4, 4], None, CAPACITY), ([-4, 0, 0], [0, 4, 4, 4], None, BAD_INDEX),
+             ([0, 0, 0], [0, 4, 4, 4], 7, BAD_INDEX), ([0, 0, 0], [0, 4, 4, 4], -1, BAD_INDEX),
+             ([0, 2 ** 31 - 2, 0], [0, 0, 4, 4], None, CAPACITY)]
+    for first, start, page, code in cases:
+        table = p.table_dev.clone()
+        if page is not None:
+            table[0, 0] = 10 ** 6 if page > 0 else page
+        p.status.zero_()
+        p.cache.write(k, k, table, _i32(first), _i32(start), status=p.status)
+        assert int(p.status) == code, (first, page)
+        p.cache.write(k, k, table, _i32(first), _i32(start))           # without a status word
+        for a, b in zip(p.big, old):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        p.status.zero_()
+        x, y = torch.ones_like(k), torch.ones_like(k)
+        p.cache.read(x, y, table, _i32(first), _i32(start), status=p.status)
+        assert int(p.status) == code and not x.any() and not y.any()
+
+
+# ------------------------------------------------------------------ attention
+
+LENS = [0, 1, 2, 3, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 300]
+SHAPES = [(1, 1, 64, 16), (8, 1, 64, 32), (2, 2, 128, 16), (32, 4, 128, 64), (4, 4, 128, 128), (6, 2, 64, 256),
+          (15, 3, 128, 32), (7, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("hq,hkv,dim,page", SHAPES)
+def test_attention_of_many_lengths(fmt, T, hq, hkv, dim, page):
+    p = Pool(LENS, fmt, hkv, dim, page, seed=T)
+    p.append(LENS)
+    q = _query(p.rng, len(LENS), T, hq, dim)
+    p.check(q, *p.attend(q))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T,hq,hkv,dim,n", [(1, 32, 4, 128, 5003), (4, 8, 1, 64, 4097), (3, 16, 2, 128, 9001), (1, 1, 1, 64, 20000)])
+def test_attention_of_one_long_sequence(fmt, T, hq, hkv, dim, n):
+    p = Pool([n], fmt, hkv, dim, 64, seed=n)
+    p.append([n])
+    q = _query(p.rng, 1, T, hq, dim)
+    p.check(q, *p.attend(q))
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_attention_with_large_logits_and_small_or_large_values(fmt):
+    """Weights from 1 down past f32's range; rows whose sizes differ by orders of magnitude."""
+    counts = [70, 200]
+    p = Pool(counts, fmt, 2, 128, 16, seed=5)
+    k, v = p.random_rows(counts)
+    v = (v * np.exp2(p.rng.integers(-12, 12, (270, 2, 1)))).astype(np.float16)
+    k[10:14] *= 20
+    p.append(counts, (k, v))
+    q = _query(p.rng, 2, 2, 16, 128, scale=8.0)
+    p.check(q, *p.attend(q))
+
+
+def test_attention_of_constant_rows():
+    """Equal keys: every cell has the same weight; equal values come back as they are."""
+    p = Pool([1000], "f16", 1, 64, 16)
+    k, v = np.ones((1000, 1, 64), np.float16), np.full((1000, 1, 64), 3.0, np.float16)
+    p.append([1000], (k, v))
+    q = np.full((1, 1, 8, 64), -30000.0, np.float16)    # every logit is the same huge negative number
+    out, lse = p.attend(q)
+    assert torch.allclose(out, torch.full_like(out, 3.0), rtol=1e-6)
+    z = -30000.0 * 64 / 8
+    assert abs(float(lse[0, 0, 0]) - (z + np.log(1000))) <= 2 * abs(z) * UNIT
+
+
+def test_a_logit_that_overflows_to_minus_infinity_has_no_weight():
+    """q k beyond f32 is not reachable from f16 rows, but infinite keys are: -inf logits drop
+    out, and a sequence with nothing else is empty."""
+    p = Pool([20, 20], "f16", 1, 64, 16)
+    k, v = p.random_rows([20, 20])
+    k[5:9] = 0
+    k[5:9, :, 0] = -np.inf
+    k[20:] = 0
+    k[20:, :, 0] = -np.inf
+    p.append([20, 20], (k, v))
+    q = np.abs(_query(p.rng, 2, 1, 4, 64)) + np.float16(0.1)
+    out, lse = p.attend(q)
+    keep = [c for c in range(20) if not 5 <= c < 9]
+    kk, vv = p.values(0)
+    assert_attention(out[0].cpu().numpy().astype(np.float64), lse[0].cpu().numpy().astype(np.float64), q[0], kk[keep], vv[keep])
+    assert not out[1].any() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("T", [2, 4])
+def test_what_a_query_does_not_see_does_not_matter(fmt, T):
+    """NaN and infinite rows among the newest tokens: queries before them are exact."""
+    counts = [90, 16, 17, T, 33]
+    for bad in range(1, T):         # the first of the newest T that holds no numbers
+        p = Pool(counts, fmt, 2, 128, 16, seed=T)
+        k, v = p.random_rows(counts)
+        at = 0
+        for c in counts:
+            for x in (k, v):
+                x[at + c - T + bad] = np.nan
+                if bad + 1 < T:
+                    x[at + c - T + bad + 1] = np.inf
+            at += c
+        p.append(counts, (k, v))
+        q = _query(p.rng, len(counts), T, 8, 128)
+        out, lse = p.attend(q)
+        for i, c in enumerate(counts):
+            kk, vv = p.values(i)
+            n = c - T + bad
+            if n == 0:
+                continue
+            assert_attention(out[i, :bad].cpu().numpy().astype(np.float64), lse[i, :bad].cpu().numpy().astype(np.float64),
+                             q[i, :bad], kk[:n], vv[:n], what=f"bad {bad} of {c}")
+            assert torch.isnan(out[i, bad:]).any(-1).all()      # those that see them say so
+
+
+def test_scale_strides_and_no_lse():
+    p = Pool([100, 40, 7], "fp8", 2, 64, 32, gap=2)
+    p.append([100, 40, 7])
+    q = _query(p.rng, 3, 2, 8, 64)
+    p.check(q, *p.attend(q, sm_scale=0.3), sm_scale=0.3)
+    wide = torch.zeros(3, 2, 12, 64, dtype=torch.float16, device="cuda")     # q of a fused projection
+    wide[:, :, :8] = H.to_dev(q)
+    a, la = p.attend(wide[:, :, :8])
+    b, lb = p.attend(q)
+    c, _ = p.attend(q, lse=False)
+    assert torch.equal(a, b) and torch.equal(la, lb) and torch.equal(c, b)
+
+
+def test_bad_lengths_and_pages_are_reported():
+    p = Pool([64, 64, 64], "f16", 1, 64, 16)
+    p.append([64, 64, 64])
+    q = _query(p.rng, 3, 1, 4, 64)
+    for lens, code in (([64, -5, 10], BAD_INDEX), ([64, 65, 10], CAPACITY), ([64, 2 ** 31 - 1, 10], CAPACITY)):
+        p.status.zero_()
+        out, lse = p.attend(q, lens=lens)
+        assert int(p.status) == code
+        for i in (0, 2):
+            k, v = p.values(i)
+            assert_attention(out[i].cpu().numpy().astype(np.float64), lse[i].cpu().numpy().astype(np.float64), q[i],
+                             k[:lens[i]], v[:lens[i]])
+        if lens[1] < 0:
+            assert not out[1].any() and torch.isneginf(lse[1]).all()
+    for bad in (-1, len(p.big[0]), 2 ** 31 - 1):
+        p.status.zero_()
+        table = p.table_dev.clone()
+        table[0, 1] = bad       # cells 16..31 of sequence 0 are skipped
+        out = torch.empty(3, 1, 4, 64, device="cuda")
+        lse = torch.empty(3, 1, 4, device="cuda")
+        ws = torch.empty(p.cache.workspace_bytes(4, 1), dtype=torch.uint8, device="cuda")
+        p.cache.attend(H.to_dev(q), table, _i32(p.lens), out, ws, lse=lse, status=p.status)
+        assert int(p.status) == BAD_INDEX
+        for i in range(3):
+            keep = [c for c in range(64) if i or not 16 <= c < 32]
+            k, v = p.values(i)
+            assert_attention(out[i].cpu().numpy().astype(np.float64), lse[i].cpu().numpy().astype(np.float64), q[i], k[keep], v[keep])
+    p.status.zero_()
+
+
+@pytest.mark.parametrize("S,top", [(200, 90), (1000, 40)])
+def test_large_batches(S, top):
+    rng = np.random.default_rng(S)
+    lens = [int(x) for x in rng.integers(0, top, S)]
+    p = Pool(lens, "fp8", 2, 64, 16, seed=S)
+    p.append(lens)
+    q = _query(p.rng, S, 1, 4, 64)
+    p.check(q, *p.attend(q))
+
+
+def test_one_very_long_among_short_sequences():
+    lens = [1, 0, 30000, 5] + [64] * 30
+    p = Pool(lens, "int4", 1, 128, 32, seed=9)
+    p.append(lens)
+    q = _query(p.rng, len(lens), 2, 8, 128)
+    p.check(q, *p.attend(q))
+
+
+def test_pages_past_32_bit_offsets():
+    """The last pages of a pool of more than 2^32 bytes (and 2^31 elements)."""
+    n, heads, page, dim = 17000, 4, 256, 128        # 262,144 bytes a page: 4.5 GB each for K and V
+    pages = [torch.empty(n, heads, page, dim, dtype=torch.float16, device="cuda") for _ in range(2)]
+    cache = Q.PagedKV(*pages, Q.QSA_PAGE_F16)
+    table = _i32([[n - 1, 5, n - 3]])
+    k, v = (torch.randn(600, heads, dim, device="cuda").half() for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    cache.write(k, v, table, _i32([0]), _i32([0, 600]), status=status)
+    back = [torch.empty_like(k) for _ in range(2)]
+    cache.read(*back, table, _i32([0]), _i32([0, 600]), status=status)
+    assert torch.equal(back[0], k) and torch.equal(back[1], v)
+    assert torch.equal(pages[0][n - 3, 1, 600 - 513], k[599, 1])
+    q = torch.randn(1, 1, 8, dim, device="cuda").half()
+    out, lse = torch.empty(1, 1, 8, dim, device="cuda"), torch.empty(1, 1, 8, device="cuda")
+    ws = torch.empty(cache.workspace_bytes(8), dtype=torch.uint8, device="cuda")
+    cache.attend(q, table, _i32([600]), out, ws, lse=lse, status=status)
+    assert int(status) == 0
+    assert_attention(out[0].cpu().numpy().astype(np.float64), lse[0].cpu().numpy().astype(np.float64), q[0].cpu().numpy(),
+                     k.cpu().numpy().astype(np.float64), v.cpu().numpy().astype(np.float64))
+
+
+# ------------------------------------------------------------------ together
+
+def test_parts_of_a_sequence_on_several_devices_are_merged():
+    """Two caches hold halves of a sequence; qsa_cp_merge joins their (out, lse)."""
+    a, b = Pool([150], "f16", 2, 64, 16, seed=1), Pool([91], "f16", 2, 64, 16, seed=2)
+    a.append([150])
+    b.append([91])
+    q = _query(a.rng, 1, 1, 8, 64)
+    parts = [p.attend(q) for p in (a, b)]
+    o = torch.stack([x[0][0, 0] for x in parts])
+    l = torch.stack([x[1][0, 0] for x in parts])
+    out = torch.empty(8, 64, device="cuda")
+    Q.cp_merge(o, l, 2, 8, 64, out)
+    k, v = (np.concatenate([x, y]) for x, y in zip(a.values(0), b.values(0)))
+    want, want_lse, bound, depth = P.attention(q[0], k, v)
+    assert (np.abs(out.cpu().numpy() - want[0]) <= 1e-4 * bound[0]).all()
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_serving_loop_with_drafts(fmt):
+    """Write the newest token and its drafts, attend with all of them, verify, drop the
+    rejected ones, go on: every step equals the plain forms on the accepted tokens."""
+    T, hq, hkv, dim, vocab = 4, 8, 2, 64, 97
+    p = Pool([200] * 5, fmt, hkv, dim, 16, seed=4)
+    p.append([50, 1, 0, 100, 31])
+    rng = p.rng
+    for step in range(6):
+        p.append([T] * 5)
+        q = _query(rng, 5, T, hq, dim)
+        p.check(q, *p.attend(q))
+        target = rng.dirichlet(np.full(vocab, 0.3), (5, T)).astype(np.float32)
+        draft = ((target[:, :-1] + rng.dirichlet(np.full(vocab, 0.3), (5, T - 1))) / 2).astype(np.float32)
+        tokens = np.array([[rng.choice(vocab, p=d / d.sum()) for d in s.astype(np.float64)] for s in draft], np.int32)
+        u = rng.random((5, T), np.float32)
+        acc, nxt = (torch.empty(5, dtype=torch.int32, device="cuda") for _ in range(2))
+        Q.verify_drafts(*(H.to_dev(x) for x in (target, draft, tokens, u)), acc, nxt, status=p.status)
+        want = [P.verify(target[i], draft[i], tokens[i], u[i]) for i in range(5)]
+        assert [tuple(x) for x in torch.stack([acc, nxt], 1).tolist()] == want
+        p.lens = [n - (T - 1) + m for n, (m, _) in zip(p.lens, want)]
+        for rows in p.rows:
+            for i, n in enumerate(p.lens):
+                rows[i] = rows[i][:n]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_captured_steps_replay_with_other_lengths(fmt):
+    """One graph of write + attend + read, replayed as the sequences grow and change places."""
+    S, hq, hkv, dim = 3, 8, 2, 128
+    p = Pool([300] * S, fmt, hkv, dim, 32, seed=8)
+    p.append([40, 1, 130])
+    dev = lambda *s, dtype=torch.float16: torch.zeros(*s, dtype=dtype, device="cuda")  # noqa: E731
+    k, v, q, back_k, back_v = dev(S, hkv, dim), dev(S, hkv, dim), dev(S, 1, hq, dim), dev(S, hkv, dim), dev(S, hkv, dim)
+    first, lens, out, lse = dev(S, dtype=torch.int32), dev(S, dtype=torch.int32), torch.zeros(S, 1, hq, dim, device="cuda"), torch.zeros(S, 1, hq, device="cuda")
+    table, start = p.table_dev.clone(), _i32(range(S + 1))
+    ws = torch.empty(p.cache.workspace_bytes(hq, 1), dtype=torch.uint8, device="cuda")
+
+    def step():
+        p.cache.write(k, v, table, first, start, status=p.status)
+        p.cache.attend(q, table, lens, out, ws, lse=lse, status=p.status)
+        p.cache.read(back_k, back_v, table, first, start, status=p.status)
+
+    stream = torch.cuda.Stream()
+    with torch.cuda.stream(stream):
+        first.copy_(_i32(p.lens))
+        lens.copy_(first + 1)
+        step()
+    stream.synchronize()
+    graphs = []
+    for _ in range(2):          # two graphs that share the workspace, replayed one after the other
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=stream):
+            step()
+        graphs.append(g)
+    for it in range(4):
+        kn, vn = p.random_rows([1] * S)
+        qn = _query(p.rng, S, 1, hq, dim)
+        order = p.rng.permutation(S)
+        table.copy_(_i32(p.table[order]))
+        first.copy_(_i32([p.lens[i] for i in order]))
+        lens.copy_(first + 1)
+        for d, s in ((k, kn), (v, vn), (q, qn)):
+            d.copy_(H.to_dev(s))
+        graphs[it % 2].replay()
+        torch.cuda.synchronize()
+        for j, i in enumerate(order):
+            for rows, x, got in ((p.rows[0], kn, back_k), (p.rows[1], vn, back_v)):
+                rows[i] = np.concatenate([rows[i], x[j:j + 1]])
+            p.lens[i] += 1
+            kk, vv = p.values(i)
+            assert_attention(out[j].cpu().numpy().astype(np.float64), lse[j].cpu().numpy().astype(np.float64), qn[j], kk, vv)
+            assert np.allclose(back_k[j].cpu().numpy(), kk[-1], rtol=2.0 ** -10)
+        assert int(p.status) == 0
+
+
+def test_two_streams_with_a_workspace_each():
+    pools = [Pool([6000, 5], "f16", 4, 128, 64, seed=i) for i in range(2)]
+    streams = [torch.cuda.Stream() for _ in pools]
+    data = []
+    for p in pools:
+        p.append([6000, 5])
+        q = _query(p.rng, 2, 1, 32, 128)
+        data.append((q, H.to_dev(q), torch.empty(2, 1, 32, 128, device="cuda"), torch.empty(2, 1, 32, device="cuda"),
+                     torch.empty(p.cache.workspace_bytes(32, 1), dtype=torch.uint8, device="cuda"), _i32(p.lens)))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for p, s, (_, qd, out, lse, ws, lens) in zip(pools, streams, data):
+            p.cache.attend(qd, p.table_dev, lens, out, ws, lse=lse, stream=s)
+    torch.cuda.synchronize()
+    for p, (q, _, out, lse, _, _) in zip(pools, data):
+        p.check(q, out, lse)
+
+
+def test_same_inputs_give_the_same_bits():
+    p = Pool([5000, 1, 700], "fp8", 4, 128, 16, seed=3)
+    p.append([5000, 1, 700])
+    q = _query(p.rng, 3, 4, 32, 128)
+    a, b = p.attend(q), p.attend(q)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_binding_refusals():
+    p = Pool([64], "fp8", 2, 64, 16)
+    q = torch.zeros(1, 1, 4, 64, dtype=torch.float16, device="cuda")
+    out, ws = torch.zeros(1, 1, 4, 64, device="cuda"), torch.zeros(p.cache.workspace_bytes(4), dtype=torch.uint8, device="cuda")
+    lens = _i32([1])
+    for bad in (dict(q=q.float()), dict(q=q.cpu()), dict(out=out.half()), dict(out=out[:, :, :2]), dict(lens=lens.long()),
+                dict(lens=_i32([1, 1])), dict(table=p.table_dev.long()), dict(q=q[..., ::2]),
+                dict(q=q.expand(1, 1, 4, 64)[:, :, ::2]), dict(status=torch.zeros(1, device="cuda"))):
+        a = {**dict(q=q, table=p.table_dev, lens=lens, out=out, status=p.status), **bad}
+        with pytest.raises(ValueError):
+            p.cache.attend(a["q"], a["table"], a["lens"], a["out"], ws, status=a["status"])
+    with pytest.raises(Q.QsaError):
+        p.cache.attend(q, p.table_dev, lens, out, ws[:256])
+    with pytest.raises(Q.QsaError):
+        p.cache.attend(torch.zeros(1, 1, 18, 64, dtype=torch.float16, device="cuda"), p.table_dev, lens,
+                       torch.zeros(1, 1, 18, 64, device="cuda"), ws)
+    rows = torch.zeros(3, 2, 64, dtype=torch.float16, device="cuda")
+    start = _i32([0, 3])
+    for bad in (dict(k=rows.float()), dict(k=rows[:2]), dict(k=rows[:1].expand(3, 2, 64)), dict(k=None),
+                dict(k=rows[:, :, ::2]), dict(start=start[:1]), dict(first=lens.float())):
+        a = {**dict(k=rows, first=_i32([0]), start=start), **bad}
+        with pytest.raises(ValueError):
+            p.cache.write(a["k"], rows, p.table_dev, a["first"], a["start"])
+    with pytest.raises(ValueError):
+        Q.PagedKV(p.parts[0], p.parts[1], Q.QSA_PAGE_FP8)                      # no scales
+    with pytest.raises(ValueError):
+        Q.PagedKV(p.parts[0][:1].expand(4, 2, 16, 64), p.parts[1][:4], Q.QSA_PAGE_FP8, p.parts[2][:4], p.parts[3][:4])
+    with pytest.raises(Q.QsaError):
+        z = torch.zeros(2, 2, 24, 64, dtype=torch.float16, device="cuda")
+        Q.PagedKV(z, z, Q.QSA_PAGE_F16)
+    empty = torch.zeros(0, 2, 64, dtype=torch.float16, device="cuda")
+    p.cache.write(empty, empty, p.table_dev, _i32([0]), _i32([0, 0]), status=p.status)
+    p.cache.attend(q[:0], p.table_dev[:0], lens[:0], out[:0], ws, status=p.status)
+    assert int(p.status) == 0
