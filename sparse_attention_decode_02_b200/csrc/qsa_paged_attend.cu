@@ -4,13 +4,17 @@
 // attention reads the whole context for every token, which is what the sparse path avoids.
 //   out = sum_c softmax_c(scale * q.K_c) V_c over the cells c < len - T + u + 1 of query u < T.
 // One pass over K and V with a running maximum and sum, split over the whole batch:
-//  - The (sequence, KV head) segments of a batch, cut into tiles of cells, form one list; CTA i
+//  - The (sequence, KV head) segments of a batch, cut into tiles of cells, form one list; team i
 //    of N takes the i-th N-th of it (found from seq_lens on the device), so ragged batches
-//    and single long sequences load every SM alike. A segment cut by a CTA border is written
-//    as partials (m, l, o), at most two a CTA, which paged_merge_kernel joins:
+//    and single long sequences load every SM alike. A segment cut by a border is written
+//    as partials (m, l, o), at most two a team, which paged_merge_kernel joins:
 //    sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Whole segments are written directly.
-//  - A warp takes 16 or 32 cells at a time from its own ring of asynchronous 16-byte copies in
-//    shared memory (no barrier between warps inside a segment). The products run on the tensor
+//  - One CTA an SM: two or three teams of four warps, each with its own share of the list, and
+//    a warpgroup whose warps load for one team each and leave their registers to the teams.
+//    Tiles of 64 cells come into the team's ring in shared memory (TMA tiles of a head's rows
+//    of a page, scales by bulk copies) across the segments' borders, so that the loads do not
+//    pause while a segment's results are joined. Each warp of the team takes 16 cells of a
+//    tile, with no barrier between warps inside a segment. The products run on the tensor
 //    cores, transposed: S^T = K q^T and O^T = V^T P^T, cells resp. dims as the 16 MMA rows
 //    and the (query, head) rows of the KV head as columns, so that no MMA row is padding.
 //    mma.sync rather than tcgen05: 8 to 32 columns leave the products far from any tensor
@@ -18,11 +22,17 @@
 //    registers, where mma.sync takes them and tcgen05 would want them written back.
 //  - Precision: codes are exact in f16 (e4m3 scales multiply logits and weights in f32; a 4-bit
 //    value is an f16 product by definition). A weight enters the second product as two f16
-//    terms of 2^15 p (22 bits, down to 2^-40 of the largest), which costs a second MMA and
-//    keeps the result at f32 precision. The products of each 16 or 32 cells are added to the
+//    terms of 2^7 p (22 bits, down to 2^-32 of the largest), which costs a second MMA and
+//    keeps the result at f32 precision. The products of each 16 cells are added to the
 //    running output in f32: the MMA's own sums truncate, and over a long chain that adds up.
-//  - The newest T - 1 cells are not seen by every query, and whatever they hold must not reach
-//    the others (0 * NaN is NaN): their V rows stay out of the MMA and are added one by one.
+//  - The newest T - 1 cells are not seen by every query, and an infinity or a NaN in them must
+//    not reach the others (0 * NaN is NaN): such a V row stays out of the MMA and is added to
+//    the queries that see it.
+//  - Code that runs once a segment is kept short and rolled: instructions come cold from L2
+//    at some 50 cycles each, so an unrolled copy of the tile's code for the segment's end, or
+//    a result loop unrolled over the columns, cost 19 us a segment.
+#include <type_traits>
+
 #include "qsa_paged.cuh"
 #include "qsa_sm100.cuh"
 
@@ -30,53 +40,66 @@ namespace qsa {
 
 namespace {
 
-constexpr int kPaWarps = 4;
+constexpr int kPaWarps = 4;                  // of a team
 constexpr int kPaThreads = 32 * kPaWarps;
-constexpr int kPaCtasPerSm = 2;
-constexpr int kPaTop = 32768;  // weights are scaled to f16's range: 2^15 p
+constexpr int kPaTile = 16 * kPaWarps;       // cells of a tile, 16 a warp
+constexpr int kPaMaxTeams = 1024;            // over the GPU
+// The running maximum is renewed when a logit passes it by 8 (in log 2), so that weights are
+// at most 2^8; times 2^7 they fill f16's range (below 2^16).
+constexpr float kPaSlack = 8.0f;
+constexpr float kPaTop = 128.0f;
 
-template <int FMT, int D>
+template <int FMT, int D, int NC>
 struct PaCfg {
-  static constexpr int U = FMT == QSA_PAGE_F16 ? 16 : 32;  // cells a warp takes at a time
-  static constexpr int SUBS = U / 16;
-  static constexpr int TILE = U * kPaWarps;                // cells of a CTA's tile
   static constexpr int ROW = page_row_bytes_c<FMT>(D);
   static constexpr int SROW = page_scale_bytes_c<FMT>(D);
-  static constexpr int KB = U * ROW;                       // bytes of a unit's K (V) rows
-  static constexpr int SB = U * SROW;                      // and of their scales
-  static constexpr int UNIT = 2 * KB + 2 * SB;
-  // ring depth: about 100 KB a CTA, two CTAs an SM
-  static constexpr int STAGES = 26112 / UNIT < 6 ? 26112 / UNIT : 6;
+  static constexpr int KB = kPaTile * ROW;                 // bytes of a tile's K (V) rows
+  static constexpr int SB = kPaTile * SROW;                // and of their scales
   static constexpr int KS = D / 16;                        // MMA k-steps of q.K = m-tiles of P.V
-  static_assert(STAGES >= 2, "the ring needs two units");
+  // Teams of a CTA (one CTA an SM): three with one column group, two where more columns need
+  // the registers or 256-byte rows the shared memory. A fourth resp. third warpgroup loads.
+  static constexpr int TEAMS = NC == 1 && ROW <= 128 ? 3 : 2;
+  static constexpr int THREADS = kPaThreads * (TEAMS + 1);
+  // registers a thread: at launch, and as the warpgroups split them
+  static constexpr int REGS = TEAMS == 3 ? 128 : 168;
+  static constexpr int REGS_TEAM = TEAMS == 3 ? 152 : 224, REGS_LOAD = 56;
+  static_assert(kPaThreads * (TEAMS * REGS_TEAM + REGS_LOAD) <= THREADS * REGS, "the shares add up");
+  // shared memory of a team: ring (K and V rows, then scales), joined results, queries, small things
+  static constexpr int JOIN = 8 * (D + 4) * kPaWarps * 4;
+  static constexpr int Q = NC > 1 ? KS * NC * 32 * 8 : 0;
+  static constexpr int SMALL = 4096;
+  static constexpr int BUDGET = (226 * 1024) / TEAMS - JOIN - Q - SMALL;
+  static constexpr int FIT = BUDGET / (2 * (KB + SB));
+  static constexpr int STAGES = FIT < 8 ? FIT : 8;
+  static constexpr int RING = STAGES * 2 * KB;
+  static constexpr int SRING = STAGES * 2 * SB;
+  static constexpr int BYTES = TEAMS * (RING + SRING + JOIN + Q + SMALL);
+  static_assert(STAGES >= 2, "the ring needs two tiles");
+  static_assert(KB % 1024 == 0, "swizzled tiles start on their pattern's border");
 };
 
-// What merge CTA i joins: the segment that CTA i is the first to continue.
+// What merge CTA i joins: the segment that team i is the first to continue.
 struct PaSplit {
   int seq, head;    // seq < 0: nothing
-  int first, last;  // CTAs that hold a part
-  int slot0;        // slot of the first one's part: 2 * first + (0 or 1); the others: 2 * cta
+  int first, last;  // teams that hold a part
+  int slot0;        // slot of the first one's part: 2 * first + (0 or 1); the others: 2 * team
   int pad[3];
 };
 
-__device__ __forceinline__ void cp_async(uint32_t dst, const void* src, int bytes16) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes16) : "memory");
-}
-template <int N>
-__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], %3, %2;" ::"r"(dst), "l"(src), "r"(bytes), "n"(N) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-  asm volatile(
+  asm(
       "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The same into fresh sums.
+__device__ __forceinline__ void mma0(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                     uint32_t b1) {
+  asm(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.0f));
 }
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -88,7 +111,7 @@ __device__ __forceinline__ void ldsm4_trans(uint32_t (&r)[4], uint32_t addr) {
 }
 __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   uint32_t d;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
 __device__ __forceinline__ float ex2(float x) {
@@ -117,8 +140,12 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) { return i ==
 
 // Two e4m3 codes (the low or high half of a word) as f16: exact.
 __device__ __forceinline__ uint32_t e4m3x2(uint32_t w, int high) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(high ? w >> 16 : w & 0xffffu), __NV_E4M3);
-  return uint32_t(h.x) | (uint32_t(h.y) << 16);
+  uint32_t d;
+  if (high)
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(d) : "r"(w));
+  else
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\t}" : "=r"(d) : "r"(w));
+  return d;
 }
 // Variant v of a word of eight 4-bit codes as two f16 values: bit 0 takes bytes 1 and 3 instead
 // of 0 and 2, bit 1 the high halves. 0x6400 | n is 1024 + n in f16, and 1024 + 16 n where
@@ -134,22 +161,21 @@ __device__ __forceinline__ uint32_t int4x2(uint32_t w, int v, __half2 scale) {
   return as_u32(__hmul2(h, scale));
 }
 
-// Where a 16-byte chunk of a unit's rows goes in shared memory: 128-byte lines whose chunks
-// are permuted so that the fragment reads below fall on different banks.
-template <int FMT, int D, bool IS_V>
-__device__ __forceinline__ uint32_t swizzled(uint32_t off) {
+// Where byte `off` of a tile of 128-byte lines is: TMA's 128-byte swizzle xors the index of a
+// 16-byte chunk in its line with the line's. (A line is a row of 128 bytes, 2 or 4 shorter
+// ones, or half a row of 256: the halves are tiles of their own.)
+__device__ __forceinline__ uint32_t swizzled(uint32_t off) { return off ^ ((off >> 3) & 0x70); }
+
+// Cell of a 16-cell tile that MMA row (S^T) resp. k-slot (P.V) r takes. Any order gives the
+// same sums; these keep the fragment reads of 8- and 4-bit rows off each other's banks: with
+// 128-byte rows, rows 2a and 2a + 1 of the order differ in bit 2 and every other row of it
+// has its own bits 1 and 2; with 64-byte rows they differ in bit 0 and every other row has
+// its own bits 0 and 2; with 32-byte rows four in turn are distinct mod 4.
+template <int FMT, int D>
+__device__ __forceinline__ int cell_of(int r) {
   constexpr int ROW = page_row_bytes_c<FMT>(D);
-  if constexpr (FMT == QSA_PAGE_F16) {
-    return off ^ (((off / ROW) & 7) << 4);
-  } else if constexpr (!IS_V) {
-    return ROW == 128 ? off ^ (((off >> 7) & 1) << 6) : off;
-  } else if constexpr (ROW == 128) {
-    return off ^ (((off >> 7) & 6) << 4);
-  } else if constexpr (ROW == 64) {
-    return off ^ (((off >> 7) & 3) << 5);
-  } else {
-    return off ^ (((off >> 7) & 1) << 5);
-  }
+  constexpr uint32_t order = FMT == QSA_PAGE_F16 ? 0x76543210u : ROW == 128 ? 0x37156240u : ROW == 64 ? 0x65742130u : 0x53427160u;
+  return (r & 8) | ((order >> (4 * (r & 7))) & 7);
 }
 
 // Dim of k-slot i of lane group member t (slots 2t, 2t+1, 2t+8, 2t+9) in k-step j of q.K.
@@ -185,13 +211,13 @@ __device__ __forceinline__ float v_value(const char* row, const char* scales, in
   }
 }
 
-// The work list: sequence s has tiles(s) = ceil(len / TILE) tiles for each KV head.
-struct PaPlace {
-  int seq;
-  long long base;  // index of the sequence's first tile
+// Position in the list of tiles: sequence s has ceil(len / 64) tiles for each KV head.
+struct PaCursor {
+  int seq, head, tile, nt, len;
 };
 
 // Sum over the CTA in thread order: this thread's exclusive prefix, the total in *total.
+template <int WARPS>
 __device__ __forceinline__ long long cta_scan(long long v, long long* s_warp, long long* total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   long long x = v;
@@ -205,7 +231,7 @@ __device__ __forceinline__ long long cta_scan(long long v, long long* s_warp, lo
   __syncthreads();
   long long before = 0, all = 0;
 #pragma unroll
-  for (int w = 0; w < kPaWarps; ++w) {
+  for (int w = 0; w < WARPS; ++w) {
     if (w < warp) before += s_warp[w];
     all += s_warp[w];
   }
@@ -213,36 +239,66 @@ __device__ __forceinline__ long long cta_scan(long long v, long long* s_warp, lo
   return before + x - v;
 }
 
-template <int FMT, int D, int NC>
-struct PaSmem {
-  using C = PaCfg<FMT, D>;
-  static constexpr int RING = kPaWarps * C::STAGES * C::UNIT;
-  static constexpr int OPAD = D + 4;  // floats a row of the warps' outputs, merged in the ring's memory
-  static constexpr int MERGE = kPaWarps * 8 * OPAD * 4;
-  static constexpr int Q = NC > 1 ? C::KS * NC * 32 * 8 : 0;
-  static constexpr int BYTES = (RING > MERGE ? RING : MERGE) + Q;
-  static_assert(BYTES <= 110 * 1024, "two CTAs an SM");
+// Small shared data of a team (PaCfg::SMALL bytes).
+struct PaSmall {
+  uint64_t full[8], empty[8];
+  long long base;
+  int64_t q_off[32];  // elements from the sequence's first query row to column c's
+  int64_t out_off[32];                 // output rows: from the sequence's first
+  int sees[32];       // u of column c (it sees cells < seen + u); far below 0 past the last column
+  int seq;
+  unsigned lost[8];   // of each ring slot: bit w is set if warp w's cells have no page in the pool
+  float m[kPaWarps][32], l[kPaWarps][32];  // statistics, then each warp's factor and 1 / l
+  float vtop[kPaWarps];
+  float newest[kPaWarps][QSA_MAX_QUERIES - 1][32];  // weights of the cells not every query sees
 };
+static_assert(sizeof(PaSmall) <= 4096, "PaCfg::SMALL");
 
 template <int FMT, int D, int NC>
-__global__ void __launch_bounds__(kPaThreads, kPaCtasPerSm)
-paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, PaSplit* __restrict__ splits) {
-  using C = PaCfg<FMT, D>;
-  using SM = PaSmem<FMT, D, NC>;
-  constexpr int U = C::U, SUBS = C::SUBS, KS = C::KS, STAGES = C::STAGES;
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long s_scan[kPaWarps], s_base;
-  __shared__ int s_seq;
-  __shared__ float s_m[kPaWarps][8 * NC], s_l[kPaWarps][8 * NC];
+__global__ void __launch_bounds__(PaCfg<FMT, D, NC>::THREADS, 1)
+paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, PagedView c,
+                    PagedAttendArgs a, float* __restrict__ part, PaSplit* __restrict__ splits) {
+  using C = PaCfg<FMT, D, NC>;
+  constexpr int KS = C::KS, STAGES = C::STAGES, ROW = C::ROW, SROW = C::SROW, TEAMS = C::TEAMS;
+  constexpr int ALL = C::THREADS;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  __shared__ long long s_scan[ALL / 32];
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int lane = threadIdx.x & 31, group = threadIdx.x / kPaThreads;
+  // the last warpgroup's warp i loads for team i (its warps beyond the teams have nothing to do)
+  const bool loads = group == TEAMS;
+  const int warp = (threadIdx.x >> 5) % kPaWarps, tid = threadIdx.x % kPaThreads;
+  const int team = loads ? min(warp, TEAMS - 1) : group;
+  const auto small = [&](int i) -> PaSmall& {
+    return *reinterpret_cast<PaSmall*>(smem + TEAMS * (C::RING + C::SRING + C::JOIN + C::Q) + i * C::SMALL);
+  };
+  PaSmall& sm = small(team);
+  float* const s_join = reinterpret_cast<float*>(smem + TEAMS * (C::RING + C::SRING) + team * C::JOIN);  // [warp][8 columns][D + 4]
+  uint2* const s_q = reinterpret_cast<uint2*>(smem + TEAMS * (C::RING + C::SRING + C::JOIN) + team * C::Q);
+  const uint32_t ring = sm100::smem_u32(smem) + team * C::RING;
+  const uint32_t sring = sm100::smem_u32(smem) + TEAMS * C::RING + team * C::SRING;
+
   const int G = a.n_q_heads / c.n_kv_heads, T = a.n_queries, R = G * T, Hkv = c.n_kv_heads;
-  const int cta = blockIdx.x;
+  const int n_teams = gridDim.x * TEAMS;
+  const int cta = blockIdx.x * TEAMS + team;  // the team's index in the GPU
   const long long table_cells = (long long)a.table_width << c.page_shift;
-  const uint32_t ring = sm100::smem_u32(smem) + warp * STAGES * C::UNIT;
-  unsigned char* const s_q = smem + (SM::BYTES - SM::Q);
-  const float c1 = a.sm_scale * 1.44269504088896341f;  // logits in units of log 2
 
+  if (loads && lane == 0 && warp < TEAMS) {
+    sm100::tma_prefetch_desc(&kmap);
+    sm100::tma_prefetch_desc(&vmap);
+#pragma unroll
+    for (int i = 0; i < STAGES; ++i) {
+      sm100::mbar_init(&sm.full[i], 1);
+      sm100::mbar_init(&sm.empty[i], kPaWarps);
+    }
+    sm100::fence_mbar_init();
+  }
+  if (!loads && tid < 32) {
+    const int u = tid / G, h = tid % G;
+    sm.q_off[tid] = u * a.q_stride + h * D;
+    sm.out_off[tid] = int64_t(u) * a.n_q_heads + h;
+    sm.sees[tid] = tid < R ? u : -(1 << 30);
+  }
   pdl_wait();
   pdl_launch_dependents();
 
@@ -250,35 +306,170 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
     const int n = a.seq_lens[s];
     return n < 0 ? 0 : n > table_cells ? int(table_cells) : n;
   };
-  const auto tiles = [&](int s) { return (length(s) + C::TILE - 1) / C::TILE; };
+  const auto tiles = [&](int s) { return int(((long long)length(s) + kPaTile - 1) / kPaTile); };
 
-  // ---- this CTA's part of the list ----
-  long long total = 0;
-  for (int b = 0; b < a.n_seqs; b += kPaThreads) {
-    long long sum;
-    cta_scan(b + tid < a.n_seqs ? tiles(b + tid) : 0, s_scan, &sum);
-    total += sum;
-  }
-  total *= Hkv;
-  // at least one tile each: CTAs beyond the tiles have nothing to do
-  const int N = int(min((long long)gridDim.x, total));
-  const long long lo = cta < N ? cta * total / N : 0, hi = cta < N ? (cta + 1) * total / N : 0;
-  {
-    long long before = 0;
-    for (int b = 0; b < a.n_seqs; b += kPaThreads) {
-      const long long mine = b + tid < a.n_seqs ? tiles(b + tid) : 0;
-      long long sum;
-      const long long at = (before + cta_scan(mine, s_scan, &sum)) * Hkv;
-      if (mine > 0 && at <= lo && lo < at + mine * Hkv) {
-        s_seq = b + tid;
-        s_base = at;
+  // ---- the team's part of the list: tiles [lo, hi) ----
+  long long total = 0, per = 0;
+  int N = 0, extra = 0;  // teams with work: at least one tile each
+  const auto share = [&] {
+    total *= Hkv;
+    N = int(min((long long)n_teams, total));
+    if (N == 0) return;
+    per = total >> 31 ? total / N : (long long)(unsigned(total) / unsigned(N));
+    extra = int(total - per * N);  // the first `extra` teams take one more
+  };
+  const auto start_of = [&](int i) { return i < N ? i * per + min(i, extra) : total; };
+  const auto find = [&](int s, long long mine, long long at) {
+    if (mine == 0) return;
+#pragma unroll
+    for (int i = 0; i < TEAMS; ++i) {
+      const long long first = start_of(blockIdx.x * TEAMS + i);
+      if (at <= first && first < at + mine * Hkv) {
+        small(i).seq = s;
+        small(i).base = at;
       }
+    }
+  };
+  if (a.n_seqs <= ALL) {
+    const int mine = int(threadIdx.x) < a.n_seqs ? tiles(threadIdx.x) : 0;
+    const long long at = cta_scan<ALL / 32>(mine, s_scan, &total) * Hkv;
+    share();
+    find(threadIdx.x, mine, at);
+  } else {
+    long long sum, before = 0;
+    for (int b = 0; b < a.n_seqs; b += ALL) {
+      const int s = b + threadIdx.x;
+      cta_scan<ALL / 32>(s < a.n_seqs ? tiles(s) : 0, s_scan, &sum);
+      total += sum;
+    }
+    share();
+    for (int b = 0; b < a.n_seqs; b += ALL) {
+      const int s = b + threadIdx.x, mine = s < a.n_seqs ? tiles(s) : 0;
+      const long long at = (before + cta_scan<ALL / 32>(mine, s_scan, &sum)) * Hkv;
+      find(s, mine, at);
       before += sum;
-      if (before * Hkv > lo) break;
     }
   }
-  // bad lengths and the results of sequences without cells: a CTA looks after its share
-  for (int s = cta; s < a.n_seqs; s += gridDim.x) {
+  const long long lo = start_of(cta), hi = start_of(cta + 1);
+  __syncthreads();
+  PaCursor cur;
+  cur.seq = cur.head = cur.tile = cur.nt = cur.len = 0;
+  if (lo < hi) {
+    cur.seq = sm.seq;
+    cur.len = length(cur.seq);
+    cur.nt = tiles(cur.seq);
+    const long long in = lo - sm.base;
+    cur.head = in >> 31 ? int(in / cur.nt) : int(unsigned(in) / unsigned(cur.nt));
+    cur.tile = int(in - (long long)cur.head * cur.nt);
+  }
+  const auto advance = [&](PaCursor& p) {  // to the next tile of the list (which has one)
+    if (++p.tile < p.nt) return;
+    p.tile = 0;
+    if (++p.head < Hkv) return;
+    p.head = 0;
+    do p.len = length(++p.seq);
+    while (p.len == 0);
+    p.nt = tiles(p.seq);
+  };
+
+  // =============================== loading warps ===============================
+  // Lane i < 4 looks after the tile's cells 16 i .. 16 i + 15. With pages of 32 tokens or more
+  // the first lane of a page loads all of its rows in the tile.
+  if (loads) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(C::REGS_LOAD));
+    if (warp >= TEAMS) return;
+    const int rows = min(kPaTile, 1 << c.page_shift);
+    const bool leads = lane < kPaWarps && (lane * 16) % rows == 0;
+    const auto entry = [&](const PaCursor& p) {
+      const int cell = p.tile * kPaTile + (lane * 16) / rows * rows;
+      return lane < kPaWarps && cell < p.len ? a.block_table[(long long)p.seq * a.table_width + (cell >> c.page_shift)] : 0;
+    };
+    // the pages of two tiles ahead are on their way
+    PaCursor ld = cur;
+    int page = 0, page1 = 0;
+    if (lo < hi) page = entry(ld);
+    if (lo + 1 < hi) {
+      advance(cur);
+      page1 = entry(cur);
+    }
+    int slot = 0;
+    uint32_t parity = 1;
+#pragma unroll 1
+    for (long long at = lo; at < hi; ++at) {
+      const PaCursor next = cur;
+      int page2 = 0;
+      if (at + 2 < hi) {
+        advance(cur);
+        page2 = entry(cur);
+      }
+      if (!sm100::mbar_wait(&sm.empty[slot], parity)) {
+        if (lane == 0) record_status(a.status, QSA_ERR_TIMEOUT);
+        break;  // the computing warps' waits run out as well
+      }
+      const int cell = ld.tile * kPaTile + lane * 16;
+      const bool wanted = lane < kPaWarps && cell < ld.len;
+      const bool ok = wanted && page >= 0 && page < c.n_pages;
+      const unsigned lost = __ballot_sync(0xffffffffu, wanted && !ok);
+      const int n_loads = __popc(__ballot_sync(0xffffffffu, ok && leads));
+      uint64_t* const bar = &sm.full[slot];
+      if (lane == 0) {
+        if (lost) record_status(a.status, QSA_ERR_BAD_INDEX);
+        sm.lost[slot] = lost;
+        if (n_loads == 0) sm100::mbar_arrive(bar);
+        else sm100::mbar_arrive_expect_tx(bar, n_loads * rows * 2 * (ROW + SROW));
+      }
+      __syncwarp();
+      if (ok && leads) {
+        const int row = row_in_page(c, ld.head, cell & ((1 << c.page_shift) - 1));
+        constexpr int LINE = ROW < 128 ? ROW : 128;  // bytes of a row in a line
+        const uint32_t dst = ring + slot * 2 * C::KB + lane * 16 * LINE;
+#pragma unroll
+        for (int x = 0; x < ROW / LINE; ++x) {
+          sm100::tma_load_3d(dst + x * kPaTile * 128, &kmap, x * 64, row * LINE / 128, page, bar);
+          sm100::tma_load_3d(dst + C::KB + x * kPaTile * 128, &vmap, x * 64, row * LINE / 128, page, bar);
+        }
+        if constexpr (SROW > 0) {
+          const uint32_t sdst = sring + slot * 2 * C::SB + lane * 16 * SROW;
+          const int64_t off = page * c.scale_stride + (int64_t)row * SROW;
+          sm100::bulk_load(sdst, c.ks + off, rows * SROW, bar);
+          sm100::bulk_load(sdst + C::SB, c.vs + off, rows * SROW, bar);
+        }
+      }
+      ld = next;
+      page = page1;
+      page1 = page2;
+      if (++slot == STAGES) {
+        slot = 0;
+        parity ^= 1;
+      }
+    }
+    return;
+  }
+
+  // =============================== computing warps ===============================
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_TEAM));
+  const int g = lane >> 2, t = lane & 3;
+  const float c1 = a.sm_scale * 1.44269504088896341f;  // logits in units of log 2
+  if (tid == 0) {
+    // the first team that continues a segment names the parts to merge
+    PaSplit sp;
+    sp.seq = -1;
+    if (lo < hi && cur.tile > 0) {
+      const long long b = lo - cur.tile, e = b + cur.nt;
+      const long long before = start_of(cta - 1);
+      if (before <= b) {
+        const long long border = extra * (per + 1), last = e - 1;
+        sp.seq = cur.seq;
+        sp.head = cur.head;
+        sp.first = cta - 1;
+        sp.last = int(last < border ? last / (per + 1) : extra + (last - border) / per);
+        sp.slot0 = 2 * (cta - 1) + (before < b);
+      }
+    }
+    splits[cta] = sp;
+  }
+  // bad lengths and the results of sequences without cells: a team looks after its share
+  for (int s = cta; s < a.n_seqs; s += n_teams) {
     const int n = a.seq_lens[s];
     if (tid == 0 && n < 0) record_status(a.status, QSA_ERR_BAD_INDEX);
     if (tid == 0 && n > table_cells) record_status(a.status, QSA_ERR_CAPACITY);
@@ -289,102 +480,32 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
         for (int e = tid; e < rows; e += kPaThreads) a.lse[(int64_t)s * rows + e] = -INFINITY;
     }
   }
-  __syncthreads();
-  if (lo >= hi) {
-    if (tid == 0) splits[cta].seq = -1;
-    return;
-  }
 
-  int seq = s_seq, len = length(seq), nt = (len + C::TILE - 1) / C::TILE;
-  int head = int((lo - s_base) / nt), tile0 = int((lo - s_base) % nt);
-  if (tid == 0) {
-    // the first CTA that continues a segment names the parts to merge
-    PaSplit sp;
-    sp.seq = -1;
-    if (tile0 > 0) {
-      const long long b = lo - tile0, e = b + nt;
-      const long long first = ((b + 1) * N - 1) / total, last = (e * N - 1) / total;
-      if (first == cta - 1) {
-        sp.seq = seq;
-        sp.head = head;
-        sp.first = int(first);
-        sp.last = int(last);
-        sp.slot0 = int(2 * first + (first * total / N == b ? 0 : 1));
-      }
-    }
-    splits[cta] = sp;
-  }
-
+  const int w16 = warp * 16;  // this warp's rows of a tile
+  const int pg = w16 + cell_of<FMT, D>(g);
+  const int pv0 = w16 + cell_of<FMT, D>(2 * t), pv1 = w16 + cell_of<FMT, D>(2 * t + 1);
+  int slot = 0;
+  uint32_t parity = 0;
+  bool timed_out = false;
   bool first_segment = true;
   for (long long at = lo; at < hi;) {
-    const int tile1 = int(min((long long)nt, tile0 + (hi - at)));
-    const int c0 = tile0 * C::TILE, c1_cell = min(len, tile1 * C::TILE);
-    const int seen = len - T + 1;  // cells before this one are seen by every query
+    const int tile0 = cur.tile, tile1 = int(min((long long)cur.nt, tile0 + (hi - at)));
+    const int len = cur.len, seen = len - T + 1;  // cells before `seen` are seen by every query
 
-    // ---- copies ----
-    const int my0 = c0 + warp * U;  // this warp's units: my0, my0 + TILE, ...
-    const int units = my0 < c1_cell ? (c1_cell - my0 + C::TILE - 1) / C::TILE : 0;
-    const int32_t* table = a.block_table + (long long)seq * a.table_width;
-    const auto page_of = [&](int unit, int sub) {  // -1: past the end
-      const int cell = my0 + unit * C::TILE + sub * 16;
-      return unit < units && cell < c1_cell ? table[cell >> c.page_shift] : -1;
-    };
-    int next_page[SUBS];
-    unsigned lost = 0;  // bit (ring slot, sub): its page is not in the pool
-#pragma unroll
-    for (int s = 0; s < SUBS; ++s) next_page[s] = page_of(0, s);
-    const auto issue = [&](int unit) {
-      if (unit < units) {
-        const uint32_t dst = ring + (unit % STAGES) * C::UNIT;
-        const int u0 = my0 + unit * C::TILE;
-#pragma unroll
-        for (int s = 0; s < SUBS; ++s) {
-          const int cell0 = u0 + s * 16;
-          int page = next_page[s];
-          next_page[s] = page_of(unit + 1, s);
-          int nk = min(16, len - cell0), nv = min(16, seen - cell0);  // rows to load (may be <= 0)
-          const unsigned bit = 1u << ((unit % STAGES) * SUBS + s);
-          lost &= ~bit;
-          if (nk > 0 && (page < 0 || page >= c.n_pages)) {
-            if (lane == 0) record_status(a.status, QSA_ERR_BAD_INDEX);
-            lost |= bit;
-            nk = 0;
-          }
-          if (nk <= 0) page = 0, nk = 0, nv = 0;
-          const int row = row_in_page(c, head, cell0 & ((1 << c.page_shift) - 1));
-          const char* ks = c.k + page * c.page_stride + (int64_t)row * C::ROW;
-          const char* vs = c.v + page * c.page_stride + (int64_t)row * C::ROW;
-#pragma unroll
-          for (int i = 0; i < C::ROW / 32; ++i) {
-            const uint32_t off = (i * 32 + lane) * 16;
-            const int r = off / C::ROW;
-            const uint32_t o = s * 16 * C::ROW + off;
-            cp_async(dst + swizzled<FMT, D, false>(o), r < nk ? ks + off : c.k, r < nk ? 16 : 0);
-            cp_async(dst + C::KB + swizzled<FMT, D, true>(o), r < nv ? vs + off : c.v, r < nv ? 16 : 0);
-          }
-          if constexpr (C::SROW > 0) {
-            // (a 4-bit row of zeros stands for -8 scale: no scale where no V row is loaded)
-            const bool ok = (lane & 15) < (FMT == QSA_PAGE_INT4 && lane >= 16 ? nv : nk);
-            const char* base = lane < 16 ? c.ks : c.vs;
-            const char* src = ok ? base + page * c.scale_stride + (int64_t)(row + (lane & 15)) * C::SROW : base;
-            cp_async_small<C::SROW>(dst + 2 * C::KB + (lane < 16 ? 0 : C::SB) + (s * 16 + (lane & 15)) * C::SROW, src,
-                                    ok ? C::SROW : 0);
-          }
-        }
-      }
-      cp_async_commit();
-    };
-#pragma unroll
-    for (int i = 0; i < STAGES - 1; ++i) issue(i);
-
-    // ---- queries: B fragments, column = (query, head) row of this KV head ----
-    const __half* q0 = static_cast<const __half*>(a.q) + (int64_t)seq * T * a.q_stride;
+    // queries: B fragments, column = (query, head) row of this KV head
+    const __half* const q0 = static_cast<const __half*>(a.q) + (int64_t)cur.seq * T * a.q_stride + cur.head * G * D;
     const auto q_frag = [&](int j, int col, int tt) {
       uint2 f = make_uint2(0u, 0u);
       if (col < R) {
-        const __half* q = q0 + (col / G) * a.q_stride + (head * G + col % G) * D;
-        f.x = as_u32(__halves2half2(q[q_dim<FMT, D>(j, tt, 0)], q[q_dim<FMT, D>(j, tt, 1)]));
-        f.y = as_u32(__halves2half2(q[q_dim<FMT, D>(j, tt, 2)], q[q_dim<FMT, D>(j, tt, 3)]));
+        const __half* q = q0 + sm.q_off[col];
+        if constexpr (FMT == QSA_PAGE_F16) {  // slots 2t, 2t + 1 and 2t + 8, 2t + 9
+          f.x = *reinterpret_cast<const uint32_t*>(q + q_dim<FMT, D>(j, tt, 0));
+          f.y = *reinterpret_cast<const uint32_t*>(q + q_dim<FMT, D>(j, tt, 2));
+        } else {  // four dims in turn; 4-bit slots take them as 0, 2, 1, 3
+          f = *reinterpret_cast<const uint2*>(q + q_dim<FMT, D>(j, tt, 0));
+          if constexpr (FMT == QSA_PAGE_INT4)
+            f = make_uint2(__byte_perm(f.x, f.y, 0x5410), __byte_perm(f.x, f.y, 0x7632));
+        }
       }
       return f;
     };
@@ -393,21 +514,20 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
 #pragma unroll
       for (int j = 0; j < KS; ++j) qf[j] = q_frag(j, g, t);
     } else {
-      for (int e = tid; e < KS * NC * 32; e += kPaThreads)
-        reinterpret_cast<uint2*>(s_q)[e] = q_frag(e / (32 * NC), (e / 32 % NC) * 8 + ((e & 31) >> 2), e & 3);
-      __syncthreads();
+#pragma unroll
+      for (int e = tid; e < KS * NC * 32; e += kPaThreads) s_q[e] = q_frag(e / (32 * NC), (e / 32 % NC) * 8 + g, t);
+      sm100::named_bar_sync(1 + team, kPaThreads);
     }
-    int limit[NC][2];  // cells that column 2t + i sees
-    float m[NC][2], l[NC][2], acc[KS][NC][4];
+    // Per column: exponents are taken from `base` (minus the running maximum times c1, 0 while
+    // there is none), which is renewed when a logit passes `limit`.
+    float base[NC][2], limit[NC][2], l[NC][2], acc[KS][NC][4];
     float vtop = 0x1p-60f;  // power of two, at least the largest V scale so far (e4m3)
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int col = n * 8 + 2 * t + i;
-        limit[n][i] = col < R ? seen + col / G : 0;
-        m[n][i] = -INFINITY;
-        l[n][i] = 0.0f;
+        base[n][i] = l[n][i] = 0.0f;
+        limit[n][i] = -INFINITY;
       }
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -415,198 +535,230 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
         for (int i = 0; i < 4; ++i) acc[k][n][i] = 0.0f;
     }
 
-    // ---- this warp's units ----
-    for (int unit = 0; unit < units; ++unit) {
-      cp_async_wait<STAGES - 2>();
-      __syncwarp();
-      const uint32_t uk = ring + (unit % STAGES) * C::UNIT, uv = uk + C::KB, uks = uv + C::KB, uvs = uks + C::SB;
-      const int u0 = my0 + unit * C::TILE;
+#pragma unroll 1
+    for (int tile = tile0; tile < tile1; ++tile) {
+      const int u0 = tile * kPaTile + w16;  // this warp's 16 cells
+      const uint32_t uk = ring + slot * 2 * C::KB, uv = uk + C::KB, uks = sring + slot * 2 * C::SB, uvs = uks + C::SB;
+      if (!timed_out && !sm100::mbar_wait(&sm.full[slot], parity)) {
+        timed_out = true;
+        if (lane == 0) record_status(a.status, QSA_ERR_TIMEOUT);
+      }
+      const bool gone = (sm.lost[slot] >> warp) & 1;
+      if (u0 < len && !gone) {
+        const bool whole = u0 + 16 <= seen;  // every query sees every cell
+        unsigned zero = 0, apart = 0;        // rows whose V must stay out of the MMA; those to add one by one
+        if (!whole) {
+          // Rows past the end hold anything; so may the newest cells, which only some queries
+          // see: if one holds an infinity or a NaN it is taken apart (0 * NaN is NaN).
+#pragma unroll 1
+          for (int r = max(0, seen - u0); r < 16; ++r) {
+            bool out = u0 + r >= len;
+            if (!out) {
+              bool odd = false;
+              for (int b = lane * 4; b < ROW; b += 128) {
+                const uint32_t w = lds32(uv + b / 128 * kPaTile * 128 + swizzled((w16 + r) * (ROW < 128 ? ROW : 128) + b % 128));
+                if (FMT == QSA_PAGE_F16) odd |= (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+                if (FMT == QSA_PAGE_FP8) odd |= __vcmpeq4(w & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+              }
+              if (FMT == QSA_PAGE_FP8) odd |= (lds32(uvs + (w16 + r) * 4) & 0x7f800000u) == 0x7f800000u;
+              if (FMT == QSA_PAGE_INT4 && lane * 4 < SROW) {
+                const uint32_t w = lds32(uvs + (w16 + r) * SROW + lane * 4);
+                odd |= (w & 0x7c00u) == 0x7c00u || (w & 0x7c000000u) == 0x7c000000u;
+              }
+              out = __any_sync(0xffffffffu, odd);
+              if (out) apart |= 1u << r;
+            }
+            if (!out) continue;
+            zero |= 1u << r;
+            for (int b = lane * 4; b < ROW; b += 128)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(uv + b / 128 * kPaTile * 128 +
+                  swizzled((w16 + r) * (ROW < 128 ? ROW : 128) + b % 128)), "r"(0) : "memory");
+            if (FMT == QSA_PAGE_INT4 && lane * 4 < SROW)  // (a 4-bit zero stands for -8 scale)
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(uvs + (w16 + r) * SROW + lane * 4), "r"(0) : "memory");
+          }
+          __syncwarp();
+        }
 
-      // S^T: cells g and g + 8 of each 16, columns 2t and 2t + 1
-      float s[SUBS][NC][4];
+        // S^T: cells cell_of(g) and cell_of(g + 8), columns 2t and 2t + 1
+        float s[NC][4];
+        {
+          uint4 raw[2][2];
+          __half2 ksc[2];
+          if constexpr (FMT == QSA_PAGE_FP8) {
 #pragma unroll
-      for (int sb = 0; sb < SUBS; ++sb) {
+            for (int r = 0; r < 2; ++r)
 #pragma unroll
-        for (int n = 0; n < NC; ++n)
+              for (int h = 0; h < D / 64; ++h)
+                raw[r][h] = lds128(uk + swizzled((pg + 8 * r) * ROW + h * 64 + t * 16));
+          } else if constexpr (FMT == QSA_PAGE_INT4) {
 #pragma unroll
-          for (int i = 0; i < 4; ++i) s[sb][n][i] = 0.0f;
-        uint4 raw[2][2];
-        __half2 ksc[2];
+            for (int r = 0; r < 2; ++r) {
+              if constexpr (D == 128) {
+                raw[r][0] = lds128(uk + swizzled((pg + 8 * r) * ROW + t * 16));
+              } else {
+                const uint2 w = lds64(uk + swizzled((pg + 8 * r) * ROW + t * 8));
+                raw[r][0] = make_uint4(w.x, w.y, 0u, 0u);
+              }
+              const int grp = D == 128 ? t : t >> 1;
+              const uint32_t w = lds32(uks + (pg + 8 * r) * SROW + (grp >> 1) * 4);
+              ksc[r] = as_h2(__byte_perm(w, w, (grp & 1) ? 0x3232 : 0x1010));
+            }
+          }
+#pragma unroll
+          for (int j = 0; j < KS; ++j) {
+            uint32_t f[4];
+            if constexpr (FMT == QSA_PAGE_F16) {
+              ldsm4(f, uk + (j >> 2) * kPaTile * 128 +
+                           swizzled((w16 + (lane & 15)) * 128 + (j & 3) * 32 + (lane >> 4) * 16));
+            } else if constexpr (FMT == QSA_PAGE_FP8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i) f[i] = e4m3x2(word_of(raw[i & 1][j >> 2], j & 3), i >> 1);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                f[i] = int4x2(word_of(raw[i & 1][0], j >> 1), (i >> 1) + 2 * (j & 1), ksc[i & 1]);
+            }
+#pragma unroll
+            for (int n = 0; n < NC; ++n) {
+              uint2 b;
+              if constexpr (NC == 1) b = qf[j];
+              else b = s_q[(j * NC + n) * 32 + lane];
+              if (j == 0) mma0(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
+              else mma(s[n], f[0], f[1], f[2], f[3], b.x, b.y);
+            }
+          }
+        }
+
+        // logits: times the row's scale (e4m3), masked
+        float vf[2] = {kPaTop, kPaTop};
         if constexpr (FMT == QSA_PAGE_FP8) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int h = 0; h < D / 64; ++h)
-              raw[r][h] = lds128(uk + swizzled<FMT, D, false>((sb * 16 + g + 8 * r) * D + h * 64 + t * 16));
-        } else if constexpr (FMT == QSA_PAGE_INT4) {
-#pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const int row = sb * 16 + g + 8 * r;
-            if constexpr (D == 128) {
-              raw[r][0] = lds128(uk + row * 64 + t * 16);
-            } else {
-              const uint2 w = lds64(uk + row * 32 + t * 8);
-              raw[r][0] = make_uint4(w.x, w.y, 0u, 0u);
-            }
-            const int grp = D == 128 ? t : t >> 1;
-            const uint32_t w = lds32(uks + row * C::SROW + (grp >> 1) * 4);
-            ksc[r] = (grp & 1) ? __high2half2(as_h2(w)) : __low2half2(as_h2(w));
-          }
-        }
-#pragma unroll
-        for (int j = 0; j < KS; ++j) {
-          uint32_t f[4];
-          if constexpr (FMT == QSA_PAGE_F16) {
-            ldsm4(f, uk + swizzled<FMT, D, false>((lane & 15) * C::ROW + j * 32 + (lane >> 4) * 16));
-          } else if constexpr (FMT == QSA_PAGE_FP8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) f[i] = e4m3x2(word_of(raw[i & 1][j >> 2], j & 3), i >> 1);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              f[i] = int4x2(word_of(raw[i & 1][0], j >> 1), (i >> 1) + 2 * (j & 1), ksc[i & 1]);
-          }
-#pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            uint2 b;
-            if constexpr (NC == 1) b = qf[j];
-            else b = reinterpret_cast<const uint2*>(s_q)[(j * NC + n) * 32 + lane];
-            mma(s[sb][n], f[0], f[1], f[2], f[3], b.x, b.y);
-          }
-        }
-      }
-
-      // logits, running maximum, weights
-      float vf[SUBS][2];
-      float vmax = 0.0f;
-#pragma unroll
-      for (int sb = 0; sb < SUBS; ++sb)
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          float f = c1;
-          vf[sb][r] = 1.0f;
-          if constexpr (FMT == QSA_PAGE_FP8) {
-            const int row = sb * 16 + g + 8 * r;
-            f *= __uint_as_float(lds32(uks + row * 4));
-            if (u0 + row < seen) {  // (the newest cells' scales are applied with their rows)
-              vf[sb][r] = __uint_as_float(lds32(uvs + row * 4));
-              vmax = fmaxf(vmax, vf[sb][r]);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NC; ++n)
-#pragma unroll
-            for (int i = 0; i < 2; ++i) s[sb][n][2 * r + i] *= f;
-        }
-      // cells that some query does not see, or that are not there
-#pragma unroll
-      for (int sb = 0; sb < SUBS; ++sb) {
-        const bool gone = (lost >> ((unit % STAGES) * SUBS + sb)) & 1;
-        if (gone || u0 + sb * 16 + 16 > seen) {
-#pragma unroll
-          for (int r = 0; r < 2; ++r)
+            const float f = __uint_as_float(lds32(uks + (pg + 8 * r) * 4));
+            vf[r] = __uint_as_float(lds32(uvs + (pg + 8 * r) * 4));
+            if ((zero >> (pg - w16 + 8 * r)) & 1) vf[r] = 0.0f;
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
-              for (int i = 0; i < 2; ++i)
-                if (gone || u0 + sb * 16 + g + 8 * r >= limit[n][i]) s[sb][n][2 * r + i] = -INFINITY;
+              for (int i = 0; i < 2; ++i) s[n][2 * r + i] *= f;
+          }
+          // weights enter the MMA relative to the largest V scale so far
+          if (__any_sync(0xffffffffu, fmaxf(vf[0], vf[1]) > vtop)) {
+            const float vmax = warp_max(fmaxf(vf[0], vf[1]));
+            const float top = __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u);
+            const float keep = vtop * __uint_as_float(0x7f000000u - __float_as_uint(top));
+            vtop = top;
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int n = 0; n < NC; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) acc[k][n][i] *= keep;
+          }
+          const float fv = kPaTop * __uint_as_float(0x7f000000u - __float_as_uint(vtop));  // / 2^e by its exponent
+#pragma unroll
+          for (int r = 0; r < 2; ++r) vf[r] = ((apart >> (pg - w16 + 8 * r)) & 1) ? kPaTop : vf[r] * fv;
         }
-      }
-      float fv = float(kPaTop), keep = 1.0f;
-      if constexpr (FMT == QSA_PAGE_FP8) {
+        if (!whole) {
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) vmax = fmaxf(vmax, __shfl_xor_sync(0xffffffffu, vmax, off));
-        const float top = fmaxf(vtop, __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u));
-        keep = vtop / top;  // both powers of two
-        vtop = top;
-        fv = float(kPaTop) / top;
-      }
-      float corr[NC][2];
-#pragma unroll
-      for (int n = 0; n < NC; ++n)
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          float x = -INFINITY;
-#pragma unroll
-          for (int sb = 0; sb < SUBS; ++sb) x = fmaxf(x, fmaxf(s[sb][n][i], s[sb][n][2 + i]));
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-          x = fmaxf(x, m[n][i]);
-          const float base = x == -INFINITY ? 0.0f : x;  // nothing seen yet: all weights 2^-inf = 0
-          corr[n][i] = ex2(m[n][i] - base);
-          m[n][i] = x;
-          float sum = 0.0f;
-#pragma unroll
-          for (int sb = 0; sb < SUBS; ++sb)
+          for (int n = 0; n < NC; ++n) {
+            const int2 u = *reinterpret_cast<const int2*>(&sm.sees[n * 8 + 2 * t]);
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-              const float p = ex2(s[sb][n][2 * r + i] - base);
-              sum += p;
-              s[sb][n][2 * r + i] = p * (vf[sb][r] * fv);
+              const int late = u0 + pg - w16 + 8 * r - seen;
+              if (late >= u.x) s[n][2 * r] = -INFINITY;
+              if (late >= u.y) s[n][2 * r + 1] = -INFINITY;
             }
-          l[n][i] = l[n][i] * corr[n][i] + sum;
-          corr[n][i] *= keep;
+          }
         }
 
-      // P^T as B fragments: two f16 terms of each weight
-      uint32_t ph[SUBS][NC][2], pl[SUBS][NC][2];
-#pragma unroll
-      for (int sb = 0; sb < SUBS; ++sb)
+        // a logit far above the running maximum: renew it
+        bool over = false;
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
+          for (int i = 0; i < 2; ++i) over |= fmaxf(s[n][i], s[n][2 + i]) > limit[n][i];
+        if (__any_sync(0xffffffffu, over)) {
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              float x = fmaxf(s[n][i], s[n][2 + i]);
+#pragma unroll
+              for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
+              const bool none = limit[n][i] == -INFINITY;
+              const float to = none ? -x * c1 : fminf(base[n][i], -x * c1);
+              if (x != -INFINITY) {  // (else this column has seen nothing here)
+                const float corr = none ? 0.0f : ex2(to - base[n][i]);
+                base[n][i] = to;
+                limit[n][i] = (kPaSlack - to) / c1;
+                l[n][i] *= corr;
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                  acc[k][n][i] *= corr;
+                  acc[k][n][2 + i] *= corr;
+                }
+              }
+            }
+        }
+        // weights; as B fragments of P^T: two f16 terms each
+        uint32_t ph[NC][2], pl[NC][2];
+#pragma unroll
+        for (int n = 0; n < NC; ++n) {
+#pragma unroll
+          for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const float p = ex2(fmaf(s[n][2 * r + i], c1, base[n][i]));
+              l[n][i] += p;
+              s[n][2 * r + i] = p * vf[r];
+            }
+#pragma unroll
           for (int r = 0; r < 2; ++r) {
-            const bool in = u0 + sb * 16 + g + 8 * r < seen;
-            const float x = in ? s[sb][n][2 * r] : 0.0f, y = in ? s[sb][n][2 * r + 1] : 0.0f;
+            const float x = s[n][2 * r], y = s[n][2 * r + 1];
             const __half2 h = __floats2half2_rn(x, y);
             const float2 back = __half22float2(h);
-            ph[sb][n][r] = transpose8x8(as_u32(h));
-            pl[sb][n][r] = transpose8x8(as_u32(__floats2half2_rn(x - back.x, y - back.y)));
+            ph[n][r] = transpose8x8(as_u32(h));
+            pl[n][r] = transpose8x8(as_u32(__floats2half2_rn(x - back.x, y - back.y)));
           }
+        }
 
-      // O^T += V^T P^T
-      uint4 raw[SUBS][4];
-      __half2 vsc[SUBS][4];
-      if constexpr (FMT != QSA_PAGE_F16) {
-#pragma unroll
-        for (int sb = 0; sb < SUBS; ++sb)
+        // O^T += V^T P^T
+        uint4 raw[4];
+        __half2 vsc[4];
+        if constexpr (FMT != QSA_PAGE_F16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            const int row = sb * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
-            const uint32_t at_row = uv + swizzled<FMT, D, true>(row * C::ROW + g * (C::ROW / 8));
-            if constexpr (C::ROW == 128) {
-              raw[sb][i] = lds128(at_row);
-            } else if constexpr (C::ROW == 64) {
+            const int row = ((i & 1) ? pv1 : pv0) + (i >> 1) * 8;
+            const uint32_t at_row = uv + swizzled(row * ROW + g * (ROW / 8));
+            if constexpr (ROW == 128) {
+              raw[i] = lds128(at_row);
+            } else if constexpr (ROW == 64) {
               const uint2 w = lds64(at_row);
-              raw[sb][i] = make_uint4(w.x, w.y, 0u, 0u);
+              raw[i] = make_uint4(w.x, w.y, 0u, 0u);
             } else {
-              raw[sb][i] = make_uint4(lds32(at_row), 0u, 0u, 0u);
+              raw[i] = make_uint4(lds32(at_row), 0u, 0u, 0u);
             }
             if constexpr (FMT == QSA_PAGE_INT4) {
               const int grp = D == 128 ? g >> 1 : g >> 2;
-              const uint32_t w = lds32(uvs + row * C::SROW + (grp >> 1) * 4);
-              vsc[sb][i] = (grp & 1) ? __high2half2(as_h2(w)) : __low2half2(as_h2(w));
+              const uint32_t w = lds32(uvs + row * SROW + (grp >> 1) * 4);
+              vsc[i] = as_h2(__byte_perm(w, w, (grp & 1) ? 0x3232 : 0x1010));
             }
           }
-      }
+        }
 #pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        float d[NC][4];
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-#pragma unroll
-        for (int sb = 0; sb < SUBS; ++sb) {
+        for (int k = 0; k < KS; ++k) {
+          float d[NC][4];
           uint32_t f[4];
           if constexpr (FMT == QSA_PAGE_F16) {
-            ldsm4_trans(f, uv + swizzled<FMT, D, true>(((lane >> 4) * 8 + (lane & 7)) * C::ROW + k * 32 + ((lane >> 3) & 1) * 16));
+            ldsm4_trans(f, uv + (k >> 2) * kPaTile * 128 +
+                               swizzled((w16 + (lane >> 4) * 8 + (lane & 7)) * 128 + (k & 3) * 32 + ((lane >> 3) & 1) * 16));
           } else {
             uint32_t h[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              if constexpr (FMT == QSA_PAGE_FP8) h[i] = e4m3x2(word_of(raw[sb][i], k >> 1), k & 1);
-              else h[i] = int4x2(word_of(raw[sb][i], k >> 2), k & 3, vsc[sb][i]);
+              if constexpr (FMT == QSA_PAGE_FP8) h[i] = e4m3x2(word_of(raw[i], k >> 1), k & 1);
+              else h[i] = int4x2(word_of(raw[i], k >> 2), k & 3, vsc[i]);
             }
             f[0] = __byte_perm(h[0], h[1], 0x5410);
             f[1] = __byte_perm(h[0], h[1], 0x7632);
@@ -614,55 +766,61 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
             f[3] = __byte_perm(h[2], h[3], 0x7632);
           }
 #pragma unroll
-          for (int n = 0; n < NC; ++n) {
-            mma(d[n], f[0], f[1], f[2], f[3], ph[sb][n][0], ph[sb][n][1]);
-            mma(d[n], f[0], f[1], f[2], f[3], pl[sb][n][0], pl[sb][n][1]);
-          }
+          for (int n = 0; n < NC; ++n) mma0(d[n], f[0], f[1], f[2], f[3], ph[n][0], ph[n][1]);
+#pragma unroll
+          for (int n = 0; n < NC; ++n) mma(d[n], f[0], f[1], f[2], f[3], pl[n][0], pl[n][1]);
+#pragma unroll
+          for (int n = 0; n < NC; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[k][n][i] += d[n][i];
         }
-#pragma unroll
-        for (int n = 0; n < NC; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[k][n][i] = fmaf(acc[k][n][i], corr[n][i & 1], d[n][i]);
-      }
 
-      // the newest cells, which not every query sees: one by one
-      if (u0 + U > seen && seen < len) {
-#pragma unroll
-        for (int sb = 0; sb < SUBS; ++sb)
+        if (apart) {  // rows that hold no numbers, to the queries that see them
+          const float inv = FMT == QSA_PAGE_FP8 ? __uint_as_float(0x7f000000u - __float_as_uint(vtop)) : 1.0f;
 #pragma unroll
           for (int r = 0; r < 2; ++r)
-            for (int cell = max(seen, u0 + sb * 16 + 8 * r); cell < min(len, u0 + sb * 16 + 8 * r + 8); ++cell) {
-              const int page = cell >= 0 ? table[cell >> c.page_shift] : -1;
-              const int src = ((cell - u0) & 7) * 4 + t;
-              float w[NC][2];
 #pragma unroll
-              for (int n = 0; n < NC; ++n)
+            for (int n = 0; n < NC; ++n)
 #pragma unroll
-                for (int i = 0; i < 2; ++i) w[n][i] = __shfl_sync(0xffffffffu, s[sb][n][2 * r + i], src);
-              if (page < 0 || page >= c.n_pages) continue;
-              const int row = row_in_page(c, head, cell & ((1 << c.page_shift) - 1));
-              const char* vr = c.v + page * c.page_stride + (int64_t)row * C::ROW;
-              const char* vs = C::SROW ? c.vs + page * c.scale_stride + (int64_t)row * C::SROW : nullptr;
-              const float scale = FMT == QSA_PAGE_FP8 ? *reinterpret_cast<const float*>(vs) : 1.0f;
+              for (int i = 0; i < 2; ++i) {
+                const int late = u0 + pg - w16 + 8 * r - seen;
+                if (late >= 0 && late < T - 1) sm.newest[warp][late][n * 8 + 2 * t + i] = s[n][2 * r + i] * inv;
+              }
+          __syncwarp();
+#pragma unroll 1
+          for (int r = 0; r < 16; ++r) {
+            if (!((apart >> r) & 1)) continue;
+            const int cell = u0 + r, late = cell - seen;
+            const int page = a.block_table[(long long)cur.seq * a.table_width + (cell >> c.page_shift)];
+            const int row = row_in_page(c, cur.head, cell & ((1 << c.page_shift) - 1));
+            const char* vr = c.v + page * c.page_stride + (int64_t)row * ROW;
+            const char* vs = SROW ? c.vs + page * c.scale_stride + (int64_t)row * SROW : nullptr;
+            const float scale = FMT == QSA_PAGE_FP8 ? *reinterpret_cast<const float*>(vs) : 1.0f;
 #pragma unroll
-              for (int k = 0; k < KS; ++k)
+            for (int k = 0; k < KS; ++k)
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                  const float x = v_value<FMT>(vr, vs, v_dim<FMT, D>(k, g, h)) * scale;
+              for (int h = 0; h < 2; ++h) {
+                const float x = v_value<FMT>(vr, vs, v_dim<FMT, D>(k, g, h)) * scale;
 #pragma unroll
-                  for (int n = 0; n < NC; ++n)
+                for (int n = 0; n < NC; ++n)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                      if (cell < limit[n][i]) acc[k][n][2 * h + i] = fmaf(w[n][i], x, acc[k][n][2 * h + i]);
-                }
-            }
+                  for (int i = 0; i < 2; ++i)
+                    if (late < sm.sees[n * 8 + 2 * t + i])
+                      acc[k][n][2 * h + i] = fmaf(sm.newest[warp][late][n * 8 + 2 * t + i], x, acc[k][n][2 * h + i]);
+              }
+          }
+        }
+        if (zero) sm100::fence_proxy_async_smem();  // the zeroed rows before the next copy into them
       }
       __syncwarp();
-      issue(unit + STAGES - 1);
+      if (lane == 0) sm100::mbar_arrive(&sm.empty[slot]);
+      if (++slot == STAGES) {
+        slot = 0;
+        parity ^= 1;
+      }
     }
 
-    // ---- the warps' results joined in the ring's memory ----
-    cp_async_wait<0>();
+    // ---- the warps' results joined ----
 #pragma unroll
     for (int n = 0; n < NC; ++n)
 #pragma unroll
@@ -670,143 +828,219 @@ paged_attend_kernel(PagedView c, PagedAttendArgs a, float* __restrict__ part, Pa
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
         if (g == 0) {
-          s_m[warp][n * 8 + 2 * t + i] = m[n][i];
-          s_l[warp][n * 8 + 2 * t + i] = l[n][i];
+          sm.m[warp][n * 8 + 2 * t + i] = -base[n][i];  // the maximum in log 2 units, where l > 0
+          sm.l[warp][n * 8 + 2 * t + i] = l[n][i];
         }
       }
-    __syncthreads();
-    const bool complete = tile0 == 0 && tile1 == nt;
-    float* const out_part = part + int64_t(2 * cta + (first_segment ? 0 : 1)) * R * (D + 2);
-    float* const s_o = reinterpret_cast<float*>(smem);
+    if (lane == 0) sm.vtop[warp] = FMT == QSA_PAGE_FP8 ? vtop / kPaTop : 1.0f / kPaTop;
+    sm100::named_bar_sync(1 + team, kPaThreads);
+    const bool complete = tile0 == 0 && tile1 == cur.nt;
+    float* const out_part = part + int64_t(2 * cta + (first_segment ? 0 : 1)) * R * (D + 4);
+    const int64_t out_row = int64_t(cur.seq) * T * a.n_q_heads + cur.head * G;
+    if (tid < R) {
+      // a warp that saw nothing has l = 0 (a NaN logit makes l, and then everything, NaN)
+      float M = -INFINITY, L = 0.0f;
 #pragma unroll
+      for (int w = 0; w < kPaWarps; ++w)
+        if (sm.l[w][tid] != 0.0f) M = fmaxf(M, sm.m[w][tid]);
+      float fw[kPaWarps];
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) {
+        const float lw = sm.l[w][tid];
+        fw[w] = lw == 0.0f ? 0.0f : ex2(sm.m[w][tid] - M);
+        L += fw[w] * lw;
+      }
+      const float end = complete ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
+#pragma unroll
+      for (int w = 0; w < kPaWarps; ++w) sm.m[w][tid] = fw[w] * sm.vtop[w];
+      sm.l[0][tid] = end;
+      if (!complete) {
+        out_part[tid * (D + 4) + D] = M;
+        out_part[tid * (D + 4) + D + 1] = L;
+      } else if (a.lse) {
+        a.lse[out_row + sm.out_off[tid]] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+      }
+    }
+    sm100::named_bar_sync(1 + team, kPaThreads);
+#pragma unroll 1
     for (int n = 0; n < NC; ++n) {
-      float f[2];
+      if (n > 0) sm100::named_bar_sync(1 + team, kPaThreads);
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int col = n * 8 + 2 * t + i;
-        float M = -INFINITY;
+        const float f = sm.m[warp][n * 8 + 2 * t + i];
 #pragma unroll
-        for (int w = 0; w < kPaWarps; ++w) M = fmaxf(M, s_m[w][col]);
-        // a warp that saw nothing has l = 0 (a NaN logit makes l, and then everything, NaN)
-        f[i] = s_l[warp][col] == 0.0f ? 0.0f : ex2(s_m[warp][col] - M) * (FMT == QSA_PAGE_FP8 ? vtop / kPaTop : 1.0f / kPaTop);
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+            s_join[(warp * 8 + 2 * t + i) * (D + 4) + v_dim<FMT, D>(k, g, h)] = acc[k][0][2 * h + i] * f;
       }
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          s_o[(warp * 8 + 2 * t + (i & 1)) * SM::OPAD + v_dim<FMT, D>(k, g, i >> 1)] = acc[k][n][i] * f[i & 1];
-      __syncthreads();
-      for (int e = tid; e < 8 * D; e += kPaThreads) {
-        const int cc = e / D, d = e % D, col = n * 8 + cc;
+      sm100::named_bar_sync(1 + team, kPaThreads);
+#pragma unroll 1
+      for (int e = tid; e < 8 * D / 4; e += kPaThreads) {
+        const int cc = e / (D / 4), d = e % (D / 4) * 4, col = n * 8 + cc;
         if (col >= R) break;
-        float o = 0.0f, M = -INFINITY, L = 0.0f;
+        float4 o = *reinterpret_cast<const float4*>(&s_join[cc * (D + 4) + d]);
 #pragma unroll
-        for (int w = 0; w < kPaWarps; ++w) {
-          o += s_o[(w * 8 + cc) * SM::OPAD + d];
-          M = fmaxf(M, s_m[w][col]);
+        for (int w = 1; w < kPaWarps; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(&s_join[(w * 8 + cc) * (D + 4) + d]);
+          o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
         }
-#pragma unroll
-        for (int w = 0; w < kPaWarps; ++w)
-          if (s_l[w][col] != 0.0f) L += ex2(s_m[w][col] - M) * s_l[w][col];
-        if (complete) {
-          const int64_t row = (int64_t(seq) * T + col / G) * a.n_q_heads + head * G + col % G;
-          a.out[row * D + d] = L == 0.0f ? 0.0f : o / L;
-          if (a.lse && d == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
-        } else {
-          out_part[col * (D + 2) + d] = o;
-          if (d == 0) {
-            out_part[col * (D + 2) + D] = M;
-            out_part[col * (D + 2) + D + 1] = L;
-          }
-        }
+        const float end = sm.l[0][col];
+        o.x *= end, o.y *= end, o.z *= end, o.w *= end;
+        float* const to = complete ? a.out + (out_row + sm.out_off[col]) * D : out_part + col * (D + 4);
+        *reinterpret_cast<float4*>(to + d) = o;
       }
-      __syncthreads();
+      if constexpr (NC > 1) {  // the next column group's sums into the registers of the first (one copy of this code)
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int x = 0; x + 1 < NC; ++x)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[k][x][i] = acc[k][x + 1][i];
+      }
     }
+    sm100::named_bar_sync(1 + team, kPaThreads);  // sm.m, sm.l, s_join and s_q are free
 
     // ---- next segment ----
     at += tile1 - tile0;
-    tile0 = 0;
     first_segment = false;
-    if (++head == Hkv && at < hi) {
-      head = 0;
-      do {
-        ++seq;
-        len = length(seq);
-      } while (len == 0);
-      nt = (len + C::TILE - 1) / C::TILE;
-    }
+    cur.tile = tile1 - 1;
+    if (at < hi) advance(cur);
   }
 }
 
-// CTA (i, row): joins row `row` of the parts of the segment that attend CTA i was the first
-// to continue.
+// CTA (i, row): joins row `row` of the parts of the segment that team i was the first to
+// continue. Each warp takes every fourth part, a lane 4 (2) dims of it, so that all its
+// loads are in flight at once; the weights come from the lanes that loaded the statistics.
 constexpr int kPmThreads = 128;
+constexpr int kPmWarps = kPmThreads / 32;
 
 template <int D>
 __global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(PagedAttendArgs a, const float* __restrict__ part,
                                                                  const PaSplit* __restrict__ splits, int n_kv_heads) {
-  __shared__ float s_w[2048];
-  __shared__ float s_red[kPmThreads / 32];
-  __shared__ float s_o[kPmThreads];
+  constexpr int V = D / 32;
+  __shared__ float s_o[kPmWarps][D];
+  __shared__ float s_w[kPaMaxTeams];
+  __shared__ float s_ml[kPmWarps][2];
   pdl_launch_dependents();
   pdl_wait();
   const PaSplit sp = splits[blockIdx.x];
   if (sp.seq < 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.n_q_heads / n_kv_heads, T = a.n_queries, R = G * T, col = blockIdx.y;
   const int n = sp.last - sp.first + 1;
-  const int64_t step = int64_t(R) * (D + 2);
-  const auto row_of = [&](int p) { return part + (p == 0 ? sp.slot0 : 2 * (sp.first + p)) * step + col * (D + 2); };
+  const int64_t step = int64_t(R) * (D + 4);
+  const auto row_of = [&](int p) { return part + (p == 0 ? sp.slot0 : 2 * (sp.first + p)) * step + col * (D + 4); };
+  // weights of all parts
   float M = -INFINITY;
   for (int p = threadIdx.x; p < n; p += kPmThreads) M = fmaxf(M, row_of(p)[D]);
   M = warp_max(M);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = M;
+  if (lane == 0) s_ml[warp][0] = M;
   __syncthreads();
 #pragma unroll
-  for (int w = 0; w < kPmThreads / 32; ++w) M = fmaxf(M, s_red[w]);
-  __syncthreads();
+  for (int w = 0; w < kPmWarps; ++w) M = fmaxf(M, s_ml[w][0]);
   float L = 0.0f;
   for (int p = threadIdx.x; p < n; p += kPmThreads) {
-    const float l = row_of(p)[D + 1];
-    const float w = l == 0.0f ? 0.0f : ex2(row_of(p)[D] - M);
+    const float l = row_of(p)[D + 1], w = l == 0.0f ? 0.0f : ex2(row_of(p)[D] - M);
     s_w[p] = w;
     L += w * l;
   }
   L = warp_sum(L);
-  if ((threadIdx.x & 31) == 0) s_red[threadIdx.x >> 5] = L;
+  if (lane == 0) s_ml[warp][1] = L;
   __syncthreads();
   L = 0.0f;
 #pragma unroll
-  for (int w = 0; w < kPmThreads / 32; ++w) L += s_red[w];
-  // D = 64: two halves of the CTA take every other part
-  constexpr int WAYS = kPmThreads / D;
-  const int d = threadIdx.x % D, way = threadIdx.x / D;
-  float o = 0.0f;
-#pragma unroll 8
-  for (int p = way; p < n; p += WAYS) o += s_w[p] * row_of(p)[d];
-  if constexpr (WAYS == 2) {
-    s_o[threadIdx.x] = o;
-    __syncthreads();
-    o += s_o[threadIdx.x ^ D];
-    if (way) return;
+  for (int w = 0; w < kPmWarps; ++w) L += s_ml[w][1];
+  float o[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) o[i] = 0.0f;
+  constexpr int B = 10;  // parts in flight
+  for (int p0 = warp; p0 < n; p0 += kPmWarps * B) {
+    float x[B][V];
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int p = p0 + b * kPmWarps;
+#pragma unroll
+      for (int i = 0; i < V; ++i) x[b][i] = 0.0f;
+      if (p < n) {
+        if constexpr (V == 4) *reinterpret_cast<float4*>(x[b]) = reinterpret_cast<const float4*>(row_of(p))[lane];
+        else *reinterpret_cast<float2*>(x[b]) = reinterpret_cast<const float2*>(row_of(p))[lane];
+      }
+    }
+#pragma unroll
+    for (int b = 0; b < B; ++b) {
+      const int p = p0 + b * kPmWarps;
+      const float w = p < n ? s_w[p] : 0.0f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) o[i] += w * x[b][i];
+    }
   }
+#pragma unroll
+  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
+  __syncthreads();
   const int64_t row = (int64_t(sp.seq) * T + col / G) * a.n_q_heads + sp.head * G + col % G;
-  a.out[row * D + d] = L == 0.0f ? 0.0f : o / L;
-  if (a.lse && d == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+  if (threadIdx.x < D) {
+    float sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kPmWarps; ++w) sum += s_o[w][threadIdx.x];
+    a.out[row * D + threadIdx.x] = L == 0.0f ? 0.0f : sum / L;
+  }
+  if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
 }
 
-int paged_ctas(int n_sms) { return n_sms * kPaCtasPerSm < 2048 ? n_sms * kPaCtasPerSm : 2048; }
+int paged_ctas(int n_sms, int teams) { return min(n_sms, kPaMaxTeams / teams); }
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// TMA descriptor of K or V pages as (128-byte lines, a page's lines, pages), or with 128-dim
+// f16 rows (row, a page's rows, pages); a tile holds `rows` rows resp. halves of rows.
+cudaError_t encode_pages(const PagedView& c, int format, void* pages, int rows, CUtensorMap* out) {
+  static const EncodeTiledFn fn = [] {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &p, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeTiledFn>(p);
+  }();
+  if (!fn) return cudaErrorNotSupported;
+  const bool f16 = format == QSA_PAGE_F16;
+  const int bytes = page_row_bytes(format, c.head_dim), line = max(bytes, 128), per_line = line / bytes;
+  const cuuint64_t dims[3] = {cuuint64_t(f16 ? line / 2 : line), (cuuint64_t(c.n_kv_heads) << c.page_shift) / per_line,
+                              cuuint64_t(c.n_pages)};
+  const cuuint64_t strides[2] = {cuuint64_t(line), cuuint64_t(c.page_stride)};
+  const cuuint32_t box[3] = {f16 ? 64u : 128u, cuuint32_t(rows / per_line), 1};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = fn(out, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, pages, dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
 
 template <int FMT, int D, int NC>
 cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, cudaStream_t s) {
-  using SM = PaSmem<FMT, D, NC>;
+  using C = PaCfg<FMT, D, NC>;
   const auto kernel = paged_attend_kernel<FMT, D, NC>;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, SM::BYTES);
+  // the warpgroups' shares come out of what the launch allocates (a larger sum would wait for
+  // registers for good)
+  static const int regs = [&] {
+    cudaFuncAttributes f;
+    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
+  }();
+  if (regs < C::REGS) return cudaErrorInvalidConfiguration;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveoutMaxShared);
+  CUtensorMap kmap, vmap;
+  const int rows = min(kPaTile, 1 << c.page_shift);
+  if (e == cudaSuccess) e = encode_pages(c, FMT, c.k, rows, &kmap);
+  if (e == cudaSuccess) e = encode_pages(c, FMT, c.v, rows, &vmap);
   if (e != cudaSuccess) return e;
-  const int n = paged_ctas(n_sms), R = a.n_q_heads / c.n_kv_heads * a.n_queries;
+  const int ctas = paged_ctas(n_sms, C::TEAMS), n = ctas * C::TEAMS, R = a.n_q_heads / c.n_kv_heads * a.n_queries;
   PaSplit* splits = static_cast<PaSplit*>(a.workspace);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align256(n * sizeof(PaSplit)));
-  e = launch_pdl(kernel, dim3(n), dim3(kPaThreads), SM::BYTES, s, 1, c, a, part, splits);
+  e = launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::BYTES, s, 1, kmap, vmap, c, a, part, splits);
   if (e != cudaSuccess) return e;
   return launch_pdl(paged_merge_kernel<D>, dim3(n, R), dim3(kPmThreads), 0, s, 1, a, (const float*)part,
                     (const PaSplit*)splits, c.n_kv_heads);
@@ -825,17 +1059,22 @@ cudaError_t launch_pa_cols(const PagedView& c, const PagedAttendArgs& a, int n_s
 
 }  // namespace
 
+constexpr int kPaMostTeams = 3;  // the largest PaCfg::TEAMS
+
 size_t paged_workspace_bytes(int head_dim, int n_q_heads, int n_kv_heads, int n_queries, int n_sms) {
-  const size_t n = paged_ctas(n_sms), R = size_t(n_q_heads) / n_kv_heads * n_queries;
-  return align256(n * sizeof(PaSplit)) + align256(2 * n * R * (head_dim + 2) * sizeof(float));
+  const size_t n = min(n_sms * kPaMostTeams, kPaMaxTeams), R = size_t(n_q_heads) / n_kv_heads * n_queries;
+  return align256(n * sizeof(PaSplit)) + align256(2 * n * R * (head_dim + 4) * sizeof(float));
 }
 
 cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, cudaStream_t s) {
   const bool wide = c.head_dim == 128;
   switch (format) {
-    case QSA_PAGE_F16: return wide ? launch_pa_cols<QSA_PAGE_F16, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_F16, 64>(c, a, n_sms, s);
-    case QSA_PAGE_FP8: return wide ? launch_pa_cols<QSA_PAGE_FP8, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_FP8, 64>(c, a, n_sms, s);
-    case QSA_PAGE_INT4: return wide ? launch_pa_cols<QSA_PAGE_INT4, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_INT4, 64>(c, a, n_sms, s);
+    case QSA_PAGE_F16:
+      return wide ? launch_pa_cols<QSA_PAGE_F16, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_F16, 64>(c, a, n_sms, s);
+    case QSA_PAGE_FP8:
+      return wide ? launch_pa_cols<QSA_PAGE_FP8, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_FP8, 64>(c, a, n_sms, s);
+    case QSA_PAGE_INT4:
+      return wide ? launch_pa_cols<QSA_PAGE_INT4, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_INT4, 64>(c, a, n_sms, s);
     default: return cudaErrorInvalidValue;
   }
 }

@@ -6,9 +6,10 @@ logit is an f32 sum of D exact products, off by at most D f32 units (2^-23, a tr
 sum) of sum|q k|, and its exponential by two units more; that error e enters numerator
 and denominator; the sums over n cells add at most n units, the rest of the chain (scale,
 split f16 weights, merge) a few tens of units. A weight is held as two f16 terms of
-2^15 p, p <= 1 relative to the largest: what is below half an f16 subnormal step of them,
-2^-25 2^-15, is lost, so each of the n weights is off by 2^-40 at most (this term counts
-where an output's own weights are all tiny).
+2^7 p, where the running maximum that p is relative to lags the largest logit by up to 2^8:
+what is below half an f16 subnormal step of them, 2^-25 2^-7, is lost, so each of the n
+weights is off by 2^-32 of the largest at most (this term counts where an output's own
+weights are all tiny).
 """
 import numpy as np
 import pytest
@@ -110,7 +111,7 @@ def assert_attention(out, lse, q, k, v, sm_scale=None, what=""):
     want, want_lse, bound, depth = P.attention(q, k, v, sm_scale)
     n, D = len(k), q.shape[-1]
     e = (D * depth + 8 * (np.abs(np.where(np.isfinite(want_lse), want_lse, 0)) + depth + 1)) * UNIT
-    tol = (2 * e[..., None] + (n + 64) * UNIT) * bound + n * 2.0 ** -40 * np.abs(v).max(initial=0.0)
+    tol = (2 * e[..., None] + (n + 64) * UNIT) * bound + n * 2.0 ** -32 * np.abs(v).max(initial=0.0)
     assert np.isfinite(out).all(), f"{what}: out is not finite"
     assert (np.abs(out - want) <= tol).all(), f"{what}: {np.max(np.abs(out - want) / np.maximum(tol, 1e-30)):.3g} of tolerance"
     empty = np.isinf(want_lse)
@@ -184,11 +185,10 @@ def test_rows_of_a_fused_projection_and_special_values():
     for fmt in FORMATS:
         p = Pool([64], fmt, 2, 128, 16)
         fused = torch.randn(40, 1024, device="cuda").half()
-        rows = fused.cpu().numpy()
         k, v = fused[:, 512:768].unflatten(1, (2, 128)), fused[:, 768:].unflatten(1, (2, 128))
         fused[3, 512:640] = 0
         fused[4, 512:520] = 6e-8
-        fused[5, 512:640] *= 2e4
+        fused[5, 512:640] = (fused[5, 512:640].float() * 2e4).clamp(-65504, 65504).half()     # huge, not infinite
         fused[6, 520] = float("inf")
         fused[7, 600] = float("nan")
         fused[8, 512:640] = 6e-8
