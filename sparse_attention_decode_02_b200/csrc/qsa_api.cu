@@ -65,10 +65,13 @@ bool usable(const void* p, size_t a) { return p && aligned(p, a); }
 
 qsa_status status_of(cudaError_t e) { return e == cudaSuccess ? QSA_OK : QSA_ERR_CUDA; }
 
-bool current_sms(int* n_sms) {
+bool current_sms(int* n_sms, int* device = nullptr) {
   int dev = 0;
-  return cudaGetDevice(&dev) == cudaSuccess &&
-         cudaDeviceGetAttribute(n_sms, cudaDevAttrMultiProcessorCount, dev) == cudaSuccess;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(n_sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return false;
+  if (device) *device = dev;
+  return true;
 }
 
 // Shape of a paged cache (the first five fields).
@@ -660,14 +663,14 @@ qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_
   if (table_width < 1 || !usable(q, 16) || !usable(block_table, 4) || !usable(seq_lens, 4) || !usable(out, 16) ||
       !aligned(lse, 4) || !usable(workspace, 256) || !aligned(status, 4))
     return QSA_ERR_INVALID_ARG;
-  int n_sms = 0;
-  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  int n_sms = 0, device = 0;
+  if (!current_sms(&n_sms, &device)) return QSA_ERR_CUDA;
   if (workspace_bytes < paged_workspace_bytes(cache->head_dim, n_q_heads, cache->n_kv_heads, n_queries, n_sms))
     return QSA_ERR_CAPACITY;
   if (sm_scale == 0.0f) sm_scale = cache->head_dim == 64 ? 0.125f : 0.088388347648318447f;
   const PagedAttendArgs a{q,        q_stride, n_queries, n_q_heads, block_table, table_width, n_seqs,
                           seq_lens, sm_scale, out,       lse,       workspace,   status};
-  return status_of(launch_paged_attend(c, cache->format, a, n_sms, (cudaStream_t)stream));
+  return status_of(launch_paged_attend(c, cache->format, a, n_sms, device, (cudaStream_t)stream));
 }
 
 qsa_status qsa_cp_index_candidates(qsa_ctx* ctx, int32_t layer, const void* q_idx, const float* w, int32_t n_global,

@@ -221,7 +221,8 @@ struct PagedAttendArgs {
   int32_t* status;
 };
 size_t paged_workspace_bytes(int head_dim, int n_q_heads, int n_kv_heads, int n_queries, int n_sms);
-cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, int device,
+                                cudaStream_t s);
 
 // ---- draft verification (qsa_verify.cu) ----
 struct VerifyArgs {

@@ -31,7 +31,7 @@
 //  - Code that runs once a segment is kept short and rolled: instructions come cold from L2
 //    at some 50 cycles each, so an unrolled copy of the tile's code for the segment's end, or
 //    a result loop unrolled over the columns, cost 19 us a segment.
-#include <type_traits>
+#include <atomic>
 
 #include "qsa_paged.cuh"
 #include "qsa_sm100.cuh"
@@ -706,15 +706,13 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
         for (int n = 0; n < NC; ++n) {
 #pragma unroll
-          for (int r = 0; r < 2; ++r)
+          for (int r = 0; r < 2; ++r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float p = ex2(fmaf(s[n][2 * r + i], c1, base[n][i]));
               l[n][i] += p;
               s[n][2 * r + i] = p * vf[r];
             }
-#pragma unroll
-          for (int r = 0; r < 2; ++r) {
             const float x = s[n][2 * r], y = s[n][2 * r + 1];
             const __half2 h = __floats2half2_rn(x, y);
             const float2 back = __half22float2(h);
@@ -725,7 +723,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
         // O^T += V^T P^T
         uint4 raw[4];
-        __half2 vsc[4];
+        __half2 vsc[2];  // 4-bit scales of cells (0, 1) and (2, 3)
         if constexpr (FMT != QSA_PAGE_F16) {
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
@@ -739,10 +737,14 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             } else {
               raw[i] = make_uint4(lds32(at_row), 0u, 0u, 0u);
             }
-            if constexpr (FMT == QSA_PAGE_INT4) {
-              const int grp = D == 128 ? g >> 1 : g >> 2;
-              const uint32_t w = lds32(uvs + row * SROW + (grp >> 1) * 4);
-              vsc[i] = as_h2(__byte_perm(w, w, (grp & 1) ? 0x3232 : 0x1010));
+          }
+          if constexpr (FMT == QSA_PAGE_INT4) {
+            const int grp = D == 128 ? g >> 1 : g >> 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x = lds32(uvs + (pv0 + 8 * i) * SROW + (grp >> 1) * 4);
+              const uint32_t y = lds32(uvs + (pv1 + 8 * i) * SROW + (grp >> 1) * 4);
+              vsc[i] = as_h2(__byte_perm(x, y, (grp & 1) ? 0x7632 : 0x5410));
             }
           }
         }
@@ -754,16 +756,20 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             ldsm4_trans(f, uv + (k >> 2) * kPaTile * 128 +
                                swizzled((w16 + (lane >> 4) * 8 + (lane & 7)) * 128 + (k & 3) * 32 + ((lane >> 3) & 1) * 16));
           } else {
-            uint32_t h[4];
+            // codes of the same dim of two cells side by side, then as f16 pairs
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              if constexpr (FMT == QSA_PAGE_FP8) h[i] = e4m3x2(word_of(raw[i], k >> 1), k & 1);
-              else h[i] = int4x2(word_of(raw[i], k >> 2), k & 3, vsc[i]);
+            for (int i = 0; i < 2; ++i) {
+              if constexpr (FMT == QSA_PAGE_FP8) {
+                const uint32_t z = __byte_perm(word_of(raw[2 * i], k >> 1), word_of(raw[2 * i + 1], k >> 1),
+                                               (k & 1) ? 0x7362 : 0x5140);
+                f[2 * i] = e4m3x2(z, 0);
+                f[2 * i + 1] = e4m3x2(z, 1);
+              } else {
+                const uint32_t x = word_of(raw[2 * i], k >> 2), y = word_of(raw[2 * i + 1], k >> 2);
+                f[2 * i] = int4x2(__byte_perm(x, y, 0x5410), k & 3, vsc[i]);
+                f[2 * i + 1] = int4x2(__byte_perm(x, y, 0x7632), k & 3, vsc[i]);
+              }
             }
-            f[0] = __byte_perm(h[0], h[1], 0x5410);
-            f[1] = __byte_perm(h[0], h[1], 0x7632);
-            f[2] = __byte_perm(h[2], h[3], 0x5410);
-            f[3] = __byte_perm(h[2], h[3], 0x7632);
           }
 #pragma unroll
           for (int n = 0; n < NC; ++n) mma0(d[n], f[0], f[1], f[2], f[3], ph[n][0], ph[n][1]);
@@ -1019,21 +1025,31 @@ cudaError_t encode_pages(const PagedView& c, int format, void* pages, int rows, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// Attributes of one kernel, set once per device. The warpgroups' shares of the registers come
+// out of what the launch allocates (a larger sum would wait for registers for good): refused
+// if the kernel was compiled for fewer.
+template <typename C, typename K>  // C: one set of flags a kernel
+cudaError_t prepare_kernel(K kernel, int smem, int regs, int device) {
+  static std::atomic<unsigned long long> ready{0};
+  const unsigned long long bit = 1ull << (device & 63);
+  if (device < 64 && (ready.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+  cudaFuncAttributes f;
+  cudaError_t e = cudaFuncGetAttributes(&f, kernel);
+  if (e == cudaSuccess && f.numRegs < regs) e = cudaErrorInvalidConfiguration;
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveoutMaxShared);
+  if (e == cudaSuccess && device < 64) ready.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int FMT, int D, int NC>
-cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, cudaStream_t s) {
+cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, int device, cudaStream_t s) {
   using C = PaCfg<FMT, D, NC>;
   const auto kernel = paged_attend_kernel<FMT, D, NC>;
-  // the warpgroups' shares come out of what the launch allocates (a larger sum would wait for
-  // registers for good)
-  static const int regs = [&] {
-    cudaFuncAttributes f;
-    return cudaFuncGetAttributes(&f, kernel) == cudaSuccess ? f.numRegs : 0;
-  }();
-  if (regs < C::REGS) return cudaErrorInvalidConfiguration;
-  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, C::BYTES);
-  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout, kCarveoutMaxShared);
+  cudaError_t e = prepare_kernel<C>(kernel, C::BYTES, C::REGS, device);
   CUtensorMap kmap, vmap;
-  const int rows = min(kPaTile, 1 << c.page_shift);
+  const int rows = min(kPaTile, 1 << c.page_shift);  // of a TMA tile
   if (e == cudaSuccess) e = encode_pages(c, FMT, c.k, rows, &kmap);
   if (e == cudaSuccess) e = encode_pages(c, FMT, c.v, rows, &vmap);
   if (e != cudaSuccess) return e;
@@ -1047,12 +1063,12 @@ cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, c
 }
 
 template <int FMT, int D>
-cudaError_t launch_pa_cols(const PagedView& c, const PagedAttendArgs& a, int n_sms, cudaStream_t s) {
+cudaError_t launch_pa_cols(const PagedView& c, const PagedAttendArgs& a, int n_sms, int device, cudaStream_t s) {
   switch ((a.n_q_heads / c.n_kv_heads * a.n_queries + 7) / 8) {
-    case 1: return launch_pa<FMT, D, 1>(c, a, n_sms, s);
-    case 2: return launch_pa<FMT, D, 2>(c, a, n_sms, s);
-    case 3: return launch_pa<FMT, D, 3>(c, a, n_sms, s);
-    case 4: return launch_pa<FMT, D, 4>(c, a, n_sms, s);
+    case 1: return launch_pa<FMT, D, 1>(c, a, n_sms, device, s);
+    case 2: return launch_pa<FMT, D, 2>(c, a, n_sms, device, s);
+    case 3: return launch_pa<FMT, D, 3>(c, a, n_sms, device, s);
+    case 4: return launch_pa<FMT, D, 4>(c, a, n_sms, device, s);
     default: return cudaErrorInvalidValue;
   }
 }
@@ -1066,15 +1082,16 @@ size_t paged_workspace_bytes(int head_dim, int n_q_heads, int n_kv_heads, int n_
   return align256(n * sizeof(PaSplit)) + align256(2 * n * R * (head_dim + 4) * sizeof(float));
 }
 
-cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, cudaStream_t s) {
+cudaError_t launch_paged_attend(const PagedView& c, int format, const PagedAttendArgs& a, int n_sms, int device,
+                                cudaStream_t s) {
   const bool wide = c.head_dim == 128;
   switch (format) {
     case QSA_PAGE_F16:
-      return wide ? launch_pa_cols<QSA_PAGE_F16, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_F16, 64>(c, a, n_sms, s);
+      return wide ? launch_pa_cols<QSA_PAGE_F16, 128>(c, a, n_sms, device, s) : launch_pa_cols<QSA_PAGE_F16, 64>(c, a, n_sms, device, s);
     case QSA_PAGE_FP8:
-      return wide ? launch_pa_cols<QSA_PAGE_FP8, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_FP8, 64>(c, a, n_sms, s);
+      return wide ? launch_pa_cols<QSA_PAGE_FP8, 128>(c, a, n_sms, device, s) : launch_pa_cols<QSA_PAGE_FP8, 64>(c, a, n_sms, device, s);
     case QSA_PAGE_INT4:
-      return wide ? launch_pa_cols<QSA_PAGE_INT4, 128>(c, a, n_sms, s) : launch_pa_cols<QSA_PAGE_INT4, 64>(c, a, n_sms, s);
+      return wide ? launch_pa_cols<QSA_PAGE_INT4, 128>(c, a, n_sms, device, s) : launch_pa_cols<QSA_PAGE_INT4, 64>(c, a, n_sms, device, s);
     default: return cudaErrorInvalidValue;
   }
 }

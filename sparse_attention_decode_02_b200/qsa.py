@@ -137,11 +137,21 @@ def _ptr(t):
     return t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream):
-    import torch
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
-    return getattr(stream, "cuda_stream", stream)
+    """Handle of `stream` (default: the current one of the current device)."""
+    global _raw_stream
+    if stream is not None:
+        return getattr(stream, "cuda_stream", stream)
+    if _raw_stream is None:
+        import torch
+        # the handle itself where torch gives it, without a Stream object around it (3 us a call)
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _raw_stream = (lambda: raw(torch._C._cuda_getDevice())) if raw and torch.cuda.is_initialized() else \
+            (lambda: torch.cuda.current_stream().cuda_stream)
+    return _raw_stream()
 
 
 def make_config(n_layers, max_ctx, d_idx, n_idx_heads, top_k_tokens, n_q_heads, n_kv_heads, head_dim,
@@ -324,20 +334,47 @@ def sparse_attend_noalloc(q, k_cache, v_cache, n_ctx, cells, n_cells, out, n_q_h
         raise QsaError(st, "qsa_sparse_attend_noalloc failed")
 
 
-def _here(*tensors):
-    """Checks that every tensor lives on the current device, where a call without a context runs."""
-    import torch
-    at = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != at:
-            raise ValueError(f"tensors must live on the current device cuda:{at} (one is on {t.device})")
+class _Types:
+    """torch's types, looked up once: the calls below check their arguments in a few attribute reads."""
+    f16 = f32 = i32 = u8 = e4m3 = device = None
+
+    @classmethod
+    def load(cls):
+        import torch
+        cls.f16, cls.f32, cls.i32, cls.u8, cls.e4m3 = (torch.float16, torch.float32, torch.int32, torch.uint8,
+                                                       torch.float8_e4m3fn)
+        cls.device = staticmethod(torch.cuda.current_device)
 
 
-def _want(name, t, dtype, shape):
-    """Checks the type and shape of an argument (None in `shape`: any size)."""
-    if t.dtype != dtype or t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)):
-        want = " x ".join("?" if w is None else str(w) for w in shape)
-        raise ValueError(f"{name} must be {dtype} of shape [{want}], got {t.dtype} {tuple(t.shape)}")
+def _bad(name, t, dtype, shape):
+    want = " x ".join("?" if w is None else str(w) for w in shape)
+    raise ValueError(f"{name} must be a {dtype} tensor of shape [{want}] on the current device, "
+                     f"got {t.dtype} {tuple(t.shape)} on {t.device}")
+
+
+def _arg(name, t, dtype, shape, device):
+    """Device pointer of a contiguous argument of this type and shape on the current device."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _bad(name, t, dtype, shape)
+    return t.data_ptr()
+
+
+def _rows_stride(name, t, dtype, shape, device):
+    """Elements between the rows of an argument whose last dims are contiguous rows and whose
+    leading dims (shape[:2] of 3 or 4) lie evenly apart; 0 if packed."""
+    if t.dtype != dtype or t.shape != shape or t.get_device() != device:
+        _bad(name, t, dtype, shape)
+    if t.is_contiguous():
+        return 0
+    st, row = t.stride(), 1
+    for n, d in zip(reversed(shape[2:]), reversed(st[2:])):
+        if n > 1 and d != row:
+            raise ValueError(f"rows of {name} must be contiguous")
+        row *= n
+    step = st[1] if shape[1] > 1 else st[0] if shape[0] > 1 else row
+    if step < row or (shape[0] > 1 and shape[1] > 1 and st[0] != shape[1] * step):
+        raise ValueError(f"rows of {name} must be equally far apart")
+    return step
 
 
 class PagedKV:
@@ -349,8 +386,10 @@ class PagedKV:
     (a layer's part of one pool: stride(0) larger than a page), the rest is contiguous."""
 
     def __init__(self, k_pages, v_pages, page_format, k_scales=None, v_scales=None):
-        import torch
+        if _Types.f32 is None:
+            _Types.load()
         self.lib = load_library()
+        self._attend = self.lib.qsa_paged_attend
         self.tensors = (k_pages, v_pages, k_scales, v_scales)  # kept alive with the descriptor
         if page_format not in (QSA_PAGE_F16, QSA_PAGE_FP8, QSA_PAGE_INT4):
             raise ValueError("page_format must be QSA_PAGE_F16, QSA_PAGE_FP8 or QSA_PAGE_INT4")
@@ -359,21 +398,21 @@ class PagedKV:
         n, heads, page, row = k_pages.shape
         self.head_dim = 2 * row if page_format == QSA_PAGE_INT4 else row
         self.n_kv_heads, self.device = heads, k_pages.get_device()
-        types = (torch.float16,) if page_format == QSA_PAGE_F16 else (torch.uint8, torch.float8_e4m3fn)
-        if page_format == QSA_PAGE_INT4:
-            types = (torch.uint8,)
-        if k_pages.dtype not in types:
-            raise ValueError(f"k_pages must be one of {types}")
-        _want("v_pages", v_pages, k_pages.dtype, (n, heads, page, row))
-        if page_format != QSA_PAGE_F16:
-            if k_scales is None or v_scales is None:
-                raise ValueError("this page format has scales")
-            shape = (n, heads, page) if page_format == QSA_PAGE_FP8 else (n, heads, page, self.head_dim // 32)
-            kind = torch.float32 if page_format == QSA_PAGE_FP8 else torch.float16
-            _want("k_scales", k_scales, kind, shape)
-            _want("v_scales", v_scales, kind, shape)
-        else:
+        types = {QSA_PAGE_F16: (_Types.f16,), QSA_PAGE_FP8: (_Types.u8, _Types.e4m3), QSA_PAGE_INT4: (_Types.u8,)}
+        want = [("k_pages", k_pages, types[page_format], (n, heads, page, row)),
+                ("v_pages", v_pages, (k_pages.dtype,), (n, heads, page, row))]
+        if page_format == QSA_PAGE_F16:
             k_scales = v_scales = None
+        elif k_scales is None or v_scales is None:
+            raise ValueError("this page format has scales")
+        else:
+            fp8 = page_format == QSA_PAGE_FP8
+            shape = (n, heads, page) if fp8 else (n, heads, page, self.head_dim // 32)
+            kind = _Types.f32 if fp8 else _Types.f16
+            want += [("k_scales", k_scales, (kind,), shape), ("v_scales", v_scales, (kind,), shape)]
+        for name, t, kinds, shape in want:
+            if t.dtype not in kinds or t.shape != shape:
+                _bad(name, t, " or ".join(map(str, kinds)), shape)
 
         def stride(a, b):  # bytes between pages; pages themselves contiguous
             if a is None:
@@ -393,25 +432,29 @@ class PagedKV:
             raise QsaError(5, "no such paged cache: page_size 16..256 (a power of two), head_dim 64 or 128")
 
     def _rows(self, k, v, block_table, first, row_start, status):
-        import torch
         a = k if k is not None else v
         if a is None:
             raise ValueError("k and v must not both be None")
+        dev = self._device()
+        n_rows, shape = a.shape[0], (1, a.shape[0], self.n_kv_heads, self.head_dim)
+        stride = _rows_stride("k", a[None], _Types.f16, shape, dev) if not a.is_contiguous() or a.dim() != 3 else 0
         for name, t in (("k", k), ("v", v)):
-            if t is not None:
-                _want(name, t, torch.float16, (a.shape[0], self.n_kv_heads, self.head_dim))
-                if t.numel() and (t.stride(2) != 1 or (self.n_kv_heads > 1 and t.stride(1) != self.head_dim) or
-                                  (t.shape[0] > 1 and (t.stride(0) != a.stride(0) or t.stride(0) < t[0].numel()))):
-                    raise ValueError("rows must be contiguous and those of k and v equally far apart")
-        n_seqs = block_table.shape[0]
-        _want("block_table", block_table, torch.int32, (n_seqs, None))
-        _want("first", first, torch.int32, (n_seqs,))
-        _want("row_start", row_start, torch.int32, (n_seqs + 1,))
-        _here(k, v, block_table, first, row_start, status, self.tensors[0])
-        stride = a.stride(0) if a.shape[0] > 1 else 0
-        return (k.data_ptr() if k is not None else None, v.data_ptr() if v is not None else None, stride,
-                a.shape[0], _ptr(block_table), block_table.shape[1], n_seqs, _ptr(first), _ptr(row_start),
-                _status_ptr(status))
+            if t is not None and (t.dtype != _Types.f16 or t.shape != shape[1:] or t.get_device() != dev or
+                                  (t is not a and t.stride() != a.stride() and n_rows > 0)):
+                _bad(name, t, _Types.f16, shape[1:])
+        n_seqs, width = block_table.shape
+        return (k.data_ptr() if k is not None else None, v.data_ptr() if v is not None else None, stride, n_rows,
+                _arg("block_table", block_table, _Types.i32, (n_seqs, width), dev), width, n_seqs,
+                _arg("first", first, _Types.i32, (n_seqs,), dev),
+                _arg("row_start", row_start, _Types.i32, (n_seqs + 1,), dev),
+                None if status is None else _arg("status", status, _Types.i32, (1,), dev))
+
+    def _device(self):
+        """The current device, which must be the cache's."""
+        dev = _Types.device()
+        if dev != self.device:
+            raise ValueError(f"the cache lives on cuda:{self.device}, the current device is cuda:{dev}")
+        return dev
 
     def write(self, k, v, block_table, first, row_start, status=None, stream=None):
         """qsa_paged_write: stores rows k, v [n_rows, n_kv_heads, head_dim] f16 (rows may lie apart)."""
@@ -438,37 +481,25 @@ class PagedKV:
 
     def attend(self, q, block_table, seq_lens, out, workspace, lse=None, sm_scale=0.0, status=None, stream=None):
         """qsa_paged_attend: q [n_seqs, n_queries, n_q_heads, head_dim] f16 (query rows may lie
-        apart evenly), out the same f32, lse [n_seqs, n_queries, n_q_heads] f32."""
-        import torch
-        n_seqs, n_queries, n_q_heads = q.shape[:3]
-        _want("q", q, torch.float16, (n_seqs, n_queries, n_q_heads, self.head_dim))
-        _want("out", out, torch.float32, (n_seqs, n_queries, n_q_heads, self.head_dim))
-        _want("block_table", block_table, torch.int32, (n_seqs, None))
-        _want("seq_lens", seq_lens, torch.int32, (n_seqs,))
-        if lse is not None:
-            _want("lse", lse, torch.float32, (n_seqs, n_queries, n_q_heads))
-        _here(q, block_table, seq_lens, out, workspace, lse, status, self.tensors[0])
-        stride = 0
-        if q.numel():
-            stride = q.stride(1) if n_queries > 1 else q.stride(0) if n_seqs > 1 else 0
-            if (not q[0, 0].is_contiguous() or (n_seqs * n_queries > 1 and stride < q[0, 0].numel()) or
-                    (n_seqs > 1 and q.stride(0) != n_queries * stride)):
-                raise ValueError("query rows must be contiguous and equally far apart")
-        st = self.lib.qsa_paged_attend(self._ref, q.data_ptr(), stride, n_queries, n_q_heads, _ptr(block_table),
-                                       block_table.shape[1], n_seqs, _ptr(seq_lens), sm_scale, _ptr(out), _ptr(lse),
-                                       _ptr(workspace), workspace.numel() * workspace.element_size(),
-                                       _status_ptr(status), _stream(stream))
+        apart evenly), out the same f32, lse [n_seqs, n_queries, n_q_heads] f32, status one i32."""
+        shape = q.shape
+        n_seqs, n_queries, n_q_heads, dim = shape
+        dev = self._device()
+        if dim != self.head_dim:
+            _bad("q", q, _Types.f16, (n_seqs, n_queries, n_q_heads, self.head_dim))
+        stride = _rows_stride("q", q, _Types.f16, shape, dev)
+        width = block_table.shape[1]
+        if workspace.get_device() != dev or not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous on the current device")
+        st = self._attend(
+            self._ref, q.data_ptr(), stride, n_queries, n_q_heads,
+            _arg("block_table", block_table, _Types.i32, (n_seqs, width), dev), width, n_seqs,
+            _arg("seq_lens", seq_lens, _Types.i32, (n_seqs,), dev), sm_scale, _arg("out", out, _Types.f32, shape, dev),
+            None if lse is None else _arg("lse", lse, _Types.f32, shape[:3], dev), workspace.data_ptr(),
+            workspace.nbytes, None if status is None else _arg("status", status, _Types.i32, (1,), dev),
+            _stream(stream))
         if st != QSA_OK:
             raise QsaError(st, "qsa_paged_attend failed")
-
-
-def _status_ptr(status):
-    if status is None:
-        return None
-    import torch
-    if status.dtype != torch.int32 or status.numel() < 1:
-        raise ValueError("status must be an int32 tensor")
-    return _ptr(status)
 
 
 def alloc_paged_kv(n_pages, page_size, n_kv_heads, head_dim, page_format=QSA_PAGE_F16, device="cuda") -> PagedKV:
@@ -491,32 +522,24 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, n_accepted,
     """qsa_verify_drafts: target_probs [n_seqs, max_drafts + 1, vocab] f32, draft_probs [n_seqs,
     max_drafts, vocab] f32 or None (rows of both may lie apart evenly), draft_tokens [n_seqs,
     max_drafts] i32, uniforms [n_seqs, max_drafts + 1] f32 -> n_accepted, next_token [n_seqs] i32."""
-    import torch
-    n_seqs, rows, vocab = target_probs.shape
+    if _Types.f32 is None:
+        _Types.load()
+    dev, shape = _Types.device(), target_probs.shape
+    n_seqs, rows, vocab = shape
     k = rows - 1
-    _want("target_probs", target_probs, torch.float32, (n_seqs, rows, vocab))
-    _want("draft_tokens", draft_tokens, torch.int32, (n_seqs, k))
-    _want("uniforms", uniforms, torch.float32, (n_seqs, rows))
-    _want("n_accepted", n_accepted, torch.int32, (n_seqs,))
-    _want("next_token", next_token, torch.int32, (n_seqs,))
-    if n_drafts is not None:
-        _want("n_drafts", n_drafts, torch.int32, (n_seqs,))
-    strides = []
-    for name, t, r in (("target_probs", target_probs, rows), ("draft_probs", draft_probs, k)):
-        if t is None or t.numel() == 0:
-            strides.append(0)
-            continue
-        _want(name, t, torch.float32, (n_seqs, r, vocab))
-        s = t.stride(1) if r > 1 else t.stride(0) if n_seqs > 1 else 0
-        if (not t[0, 0].is_contiguous() or (n_seqs * r > 1 and s < vocab) or
-                (n_seqs > 1 and t.stride(0) != r * s)):
-            raise ValueError(f"rows of {name} must be contiguous and equally far apart")
-        strides.append(s)
-    _here(target_probs, draft_probs, draft_tokens, uniforms, n_accepted, next_token, n_drafts, status)
+    t_stride = _rows_stride("target_probs", target_probs, _Types.f32, shape, dev)
+    d_ptr, d_stride = None, 0
+    if draft_probs is not None and k > 0:
+        d_stride = _rows_stride("draft_probs", draft_probs, _Types.f32, (n_seqs, k, vocab), dev)
+        d_ptr = draft_probs.data_ptr()
     st = load_library().qsa_verify_drafts(
-        target_probs.data_ptr(), strides[0], None if draft_probs is None else draft_probs.data_ptr(), strides[1],
-        _ptr(draft_tokens), _ptr(n_drafts), _ptr(uniforms), n_seqs, k, vocab, _ptr(n_accepted), _ptr(next_token),
-        _status_ptr(status), _stream(stream))
+        target_probs.data_ptr(), t_stride, d_ptr, d_stride,
+        _arg("draft_tokens", draft_tokens, _Types.i32, (n_seqs, k), dev),
+        None if n_drafts is None else _arg("n_drafts", n_drafts, _Types.i32, (n_seqs,), dev),
+        _arg("uniforms", uniforms, _Types.f32, (n_seqs, rows), dev), n_seqs, k, vocab,
+        _arg("n_accepted", n_accepted, _Types.i32, (n_seqs,), dev),
+        _arg("next_token", next_token, _Types.i32, (n_seqs,), dev),
+        None if status is None else _arg("status", status, _Types.i32, (1,), dev), _stream(stream))
     if st != QSA_OK:
         raise QsaError(st, "qsa_verify_drafts failed")
 
