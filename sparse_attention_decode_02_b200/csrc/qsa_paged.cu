@@ -5,184 +5,308 @@
 // head_dim values of one (token, KV head).
 //   e4m3: scale = amax * (1/448), code = e4m3(x * (448 * (1/amax)));
 //   4 bits: per 32 dims s = f16(amax * (1/7)), code = rint(x * (1/s)) in [-7, 7].
-// Both calls only move data: a row's 2 * head_dim f16 bytes and its stored bytes.
+// Both calls only move data: a row's 2 * head_dim f16 bytes and its stored bytes. A CTA takes
+// some tokens: it finds their places once (sequence by a count over row_start, then page), then
+// every thread moves 16-byte pieces of f16 rows, 8 values each, with several K and V pieces
+// in flight; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
 #include "qsa_paged.cuh"
-#include "qsa_pool.cuh"
 
 namespace qsa {
 
 namespace {
 
 constexpr int kRowThreads = 256;
+constexpr int kRowTokens = 64;   // most tokens a CTA takes
+constexpr int kRowBatch = 2;     // K and V pieces a thread has in flight
 
-// Where row `row` of a write or a read lives. False, after reporting it, if nowhere.
-__device__ __forceinline__ bool find_row(const PagedView& c, const PagedRows& r, int row, int lane, int* page,
-                                         int* place, bool* padding) {
-  *padding = row >= r.row_start[r.n_seqs];
-  if (*padding) return false;
-  int lo = 0, hi = r.n_seqs;  // the last sequence with row_start <= row
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (r.row_start[mid] <= row) lo = mid; else hi = mid;
+// Where a token's rows are: byte offsets of head 0's row and of its scales; rows -1: nowhere,
+// -2: padding.
+struct TokenPlace {
+  int64_t rows, scales;
+};
+
+// Finds the places of tokens [t0, t0 + n) (the whole CTA; s_at holds n of them). Two rounds of
+// dependent loads: the sequences' starts and first positions, then the pages.
+template <int FMT, int D>
+__device__ __forceinline__ void find_tokens(const PagedView& c, const PagedRows& r, int t0, int n, TokenPlace* s_at) {
+  __shared__ int s_start[kRowThreads], s_first[kRowThreads];
+  const int i = threadIdx.x, row = t0 + i;
+  const int end = r.row_start[r.n_seqs];
+  TokenPlace at{i < n && row >= end ? -2 : -1, 0};
+  int seq = -1, start = 0, first = 0;
+  for (int b = 0; b < r.n_seqs; b += kRowThreads) {
+    const int m = min(kRowThreads, r.n_seqs - b);
+    if (b > 0) __syncthreads();
+    if (i < m) {
+      s_start[i] = r.row_start[b + i];
+      s_first[i] = r.first[b + i];
+    }
+    __syncthreads();
+    if (i < n && s_start[0] <= row) {  // the last sequence that starts at or before the token
+      int lo = 0, hi = m - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (s_start[mid] <= row) lo = mid; else hi = mid - 1;
+      }
+      seq = b + lo;
+      start = s_start[lo];
+      first = s_first[lo];
+    }
   }
-  const long long pos = (long long)r.first[lo] + (row - r.row_start[lo]);
-  const long long at = pos >> c.page_shift;
-  if (row < r.row_start[lo] || pos < 0 || at >= r.table_width) {
-    if (lane == 0) record_status(r.status, pos < 0 || row < r.row_start[lo] ? QSA_ERR_BAD_INDEX : QSA_ERR_CAPACITY);
-    return false;
+  if (i < n) {
+    if (at.rows != -2) {
+      const long long pos = (long long)first + row - start, entry = pos >> c.page_shift;
+      if (seq < 0 || pos < 0) {
+        record_status(r.status, QSA_ERR_BAD_INDEX);
+      } else if (entry >= r.table_width) {
+        record_status(r.status, QSA_ERR_CAPACITY);
+      } else {
+        const int page = r.block_table[(long long)seq * r.table_width + entry];
+        if (page < 0 || page >= c.n_pages) record_status(r.status, QSA_ERR_BAD_INDEX);
+        else {
+          const int place = int(pos) & ((1 << c.page_shift) - 1);
+          at = TokenPlace{page * c.page_stride + place * page_row_bytes_c<FMT>(D),
+                          page * c.scale_stride + place * page_scale_bytes_c<FMT>(D)};
+        }
+      }
+    }
+    s_at[i] = at;
   }
-  *page = r.block_table[(long long)lo * r.table_width + at];
-  *place = int(pos) & ((1 << c.page_shift) - 1);
-  if (*page < 0 || *page >= c.n_pages) {
-    if (lane == 0) record_status(r.status, QSA_ERR_BAD_INDEX);
-    return false;
-  }
-  return true;
+  __syncthreads();
 }
 
-// One warp stores one row: lane l holds dims [l*D/32, (l+1)*D/32).
+__device__ __forceinline__ __half2 half2_at(const uint4& x, int i) {
+  const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+  return *reinterpret_cast<const __half2*>(&w);
+}
+
+// Stores piece `ch` (8 values) of the row at `dst` with its scale(s) at `scale`: all lanes take
+// part in the shuffles, `ok` ones store.
 template <int FMT, int D>
-__device__ __forceinline__ void store_row(const __half* src, char* pages, char* scales, int64_t page_base,
-                                          int64_t scale_base, int row, int lane) {
-  constexpr int P = D / 32;
-  char* dst = pages + page_base + int64_t(row) * page_row_bytes_c<FMT>(D);
+__device__ __forceinline__ void store_piece(const uint4& x, char* dst, char* scale, int ch, bool ok) {
   if constexpr (FMT == QSA_PAGE_F16) {
-    if constexpr (P == 4) reinterpret_cast<uint2*>(dst)[lane] = reinterpret_cast<const uint2*>(src)[lane];
-    else reinterpret_cast<uint32_t*>(dst)[lane] = reinterpret_cast<const uint32_t*>(src)[lane];
+    if (ok) reinterpret_cast<uint4*>(dst)[ch] = x;
   } else if constexpr (FMT == QSA_PAGE_FP8) {
-    const Fp8Row x = fp8_row_load(src, D, lane);
-    const float top = warp_max(fmaxf(fmaxf(fabsf(x.x[0]), fabsf(x.x[1])), fmaxf(fabsf(x.x[2]), fabsf(x.x[3]))));
+    __half2 h = __hmax2(__hmax2(__habs2(half2_at(x, 0)), __habs2(half2_at(x, 1))),
+                        __hmax2(__habs2(half2_at(x, 2)), __habs2(half2_at(x, 3))));
+#pragma unroll
+    for (int off = D / 16; off >= 1; off >>= 1) h = __hmax2(h, __shfl_xor_sync(0xffffffffu, h, off));
+    const float top = fmaxf(__low2float(h), __high2float(h));
     const float factor = top > 0.0f ? __fmul_rn(448.0f, 1.0f / top) : 0.0f;
-    unsigned codes = 0;
+    uint32_t codes[4];
 #pragma unroll
-    for (int i = 0; i < P; i += 2)
-      codes |= unsigned(__nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(x.x[i], factor), __fmul_rn(x.x[i + 1], factor)),
-                                                 __NV_SATFINITE, __NV_E4M3))
-               << (8 * i);
-    if constexpr (P == 4) reinterpret_cast<uint32_t*>(dst)[lane] = codes;
-    else reinterpret_cast<uint16_t*>(dst)[lane] = (unsigned short)codes;
-    if (lane == 0)
-      reinterpret_cast<float*>(scales + scale_base)[row] = top > 0.0f ? __fmul_rn(top, 1.0f / 448.0f) : 1.0f;
+    for (int i = 0; i < 4; ++i) {
+      const float2 v = __half22float2(half2_at(x, i));
+      codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v.x, factor), __fmul_rn(v.y, factor)), __NV_SATFINITE,
+                                          __NV_E4M3);
+    }
+    if (ok) {
+      reinterpret_cast<uint2*>(dst)[ch] = make_uint2(__byte_perm(codes[0], codes[1], 0x5410), __byte_perm(codes[2], codes[3], 0x5410));
+      if (ch == 0) *reinterpret_cast<float*>(scale) = top > 0.0f ? __fmul_rn(top, 1.0f / 448.0f) : 1.0f;
+    }
   } else {
-    constexpr int GL = kInt4Group / P;  // lanes of a group
-    __half x[P];
-    unsigned top = 0;  // the largest |x| as bits: NaN and infinity rank above every number
+    // the largest |x| of the group (4 lanes): a NaN or an infinity comes through
+    __half2 h = __hmax2_nan(__hmax2_nan(__habs2(half2_at(x, 0)), __habs2(half2_at(x, 1))),
+                            __hmax2_nan(__habs2(half2_at(x, 2)), __habs2(half2_at(x, 3))));
+    h = __hmax2_nan(h, __shfl_xor_sync(0xffffffffu, h, 1));
+    h = __hmax2_nan(h, __shfl_xor_sync(0xffffffffu, h, 2));
+    const __half top = __hmax_nan(__low2half(h), __high2half(h));
+    const __half s = __half_as_ushort(top) >= 0x7c00u ? __ushort_as_half(0x7fff)
+                                                      : __float2half_rn(__fmul_rn(__half2float(top), 1.0f / 7.0f));
+    const float sf = __half2float(s), inv = sf == 0.0f ? 0.0f : 1.0f / sf;
+    // rint(y) + 8 in the low bits of y + (1.5 * 2^23 + 8): the sum rounds to a whole number, to
+    // even at ties. |y| is below 7.5 unless the scale lost bits (a subnormal f16): then clamped.
+    const bool coarse = sf < 6.1e-5f;
+    uint32_t y[8];
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      x[i] = src[lane * P + i];
-      top = max(top, unsigned(__half_as_ushort(x[i]) & 0x7fff));
+    for (int i = 0; i < 8; ++i) {
+      const float2 v = __half22float2(half2_at(x, i >> 1));
+      float f = __fmul_rn((i & 1) ? v.y : v.x, inv);
+      if (coarse) f = fminf(fmaxf(f, -7.0f), 7.0f);
+      y[i] = __float_as_uint(__fadd_rn(f, 12582920.0f));
     }
+    uint32_t codes[2];
 #pragma unroll
-    for (int off = 1; off < GL; off <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, off));
-    const __half s = top >= 0x7c00u ? __ushort_as_half(0x7fff)
-                                    : __float2half_rn(__fmul_rn(__half2float(__ushort_as_half((unsigned short)top)), 1.0f / 7.0f));
-    const float sf = __half2float(s);
-    const float inv = sf == 0.0f ? 0.0f : 1.0f / sf;
-    unsigned codes = 0;
-#pragma unroll
-    for (int i = 0; i < P; ++i) {
-      const float y = rintf(__fmul_rn(__half2float(x[i]), inv));
-      codes |= unsigned(int(fminf(fmaxf(y, -7.0f), 7.0f)) + 8) << (8 * i);
+    for (int i = 0; i < 2; ++i) {
+      codes[i] = __byte_perm(__byte_perm(y[4 * i], y[4 * i + 1], 0x0040), __byte_perm(y[4 * i + 2], y[4 * i + 3], 0x0040), 0x5410);
+      codes[i] &= 0x0f0f0f0fu;
+      // dims + 16 of the group, two lanes on, into the high halves
+      codes[i] |= __shfl_down_sync(0xffffffffu, codes[i], 2) << 4;
     }
-    codes |= __shfl_down_sync(0xffffffffu, codes, GL / 2) << 4;  // dims + 16 in the high halves
-    if ((lane & (GL - 1)) < GL / 2) {
-      unsigned char* d = reinterpret_cast<unsigned char*>(dst) + (lane / GL) * 16 + (lane & (GL - 1)) * P;
-      if constexpr (P == 4) *reinterpret_cast<uint32_t*>(d) = codes;
-      else *reinterpret_cast<uint16_t*>(d) = (unsigned short)codes;
-    }
-    if ((lane & (GL - 1)) == 0)
-      (reinterpret_cast<__half*>(scales + scale_base) + int64_t(row) * (D / kInt4Group))[lane / GL] = s;
+    if (ok && (ch & 3) < 2) reinterpret_cast<uint2*>(dst + (ch >> 2) * 16)[ch & 1] = make_uint2(codes[0], codes[1]);
+    if (ok && (ch & 3) == 0) reinterpret_cast<__half*>(scale)[ch >> 2] = s;
   }
 }
 
-template <int FMT, int D>
-__device__ __forceinline__ void load_row(__half* out, const char* pages, const char* scales, int64_t page_base,
-                                         int64_t scale_base, int row, int lane) {
-  constexpr int P = D / 32;
-  const char* src = pages + page_base + int64_t(row) * page_row_bytes_c<FMT>(D);
-  __half x[P];
+// What piece `ch` of a stored row is read from, and its values.
+template <int FMT>
+struct StoredPiece {
+  uint4 codes;
+  float scale;  // e4m3
+  __half s;     // 4 bits
+};
+
+template <int FMT>
+__device__ __forceinline__ StoredPiece<FMT> load_piece(const char* src, const char* scale, int ch) {
+  StoredPiece<FMT> p{};
+  if constexpr (FMT == QSA_PAGE_F16) {
+    p.codes = reinterpret_cast<const uint4*>(src)[ch];
+  } else {
+    const uint2 w = FMT == QSA_PAGE_FP8 ? reinterpret_cast<const uint2*>(src)[ch]
+                                        : reinterpret_cast<const uint2*>(src + (ch >> 2) * 16)[ch & 1];
+    p.codes.x = w.x;
+    p.codes.y = w.y;
+    if constexpr (FMT == QSA_PAGE_FP8) p.scale = *reinterpret_cast<const float*>(scale);
+    else p.s = reinterpret_cast<const __half*>(scale)[ch >> 2];
+  }
+  return p;
+}
+
+template <int FMT>
+__device__ __forceinline__ uint4 values_of(const StoredPiece<FMT>& p, int ch) {
+  uint32_t out[4] = {p.codes.x, p.codes.y, p.codes.z, p.codes.w};
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    const int d = lane * P + i;
-    if constexpr (FMT == QSA_PAGE_F16) {
-      x[i] = reinterpret_cast<const __half*>(src)[d];
-    } else if constexpr (FMT == QSA_PAGE_FP8) {
-      const float s = (reinterpret_cast<const float*>(scales + scale_base))[row];
-      const __half c = __half(__nv_cvt_fp8_to_halfraw(reinterpret_cast<const unsigned char*>(src)[d], __NV_E4M3));
-      x[i] = __float2half_rn(__half2float(c) * s);
+  for (int i = 0; i < (FMT == QSA_PAGE_F16 ? 0 : 4); ++i) {
+    const uint32_t w = i < 2 ? p.codes.x : p.codes.y;
+    __half2 h;
+    if constexpr (FMT == QSA_PAGE_FP8) {
+      const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((w >> (16 * (i & 1))) & 0xffffu), __NV_E4M3);
+      const float2 f = __half22float2(__half2(r));
+      h = __floats2half2_rn(__fmul_rn(f.x, p.scale), __fmul_rn(f.y, p.scale));
     } else {
-      const __half s = (reinterpret_cast<const __half*>(scales + scale_base) + int64_t(row) * (D / 32))[d / 32];
-      const unsigned b = reinterpret_cast<const unsigned char*>(src)[d / 32 * 16 + d % 16];
-      x[i] = __hmul(__int2half_rn(int((d & 16) ? b >> 4 : b & 15) - 8), s);
+      // two codes as 1024 + n in f16 (0x6400 | n), minus 1032: exact
+      const uint32_t b = (__byte_perm((ch & 2) ? w >> 4 : w, 0, (i & 1) ? 0x4342 : 0x4140) & 0x000f000fu) | 0x64006400u;
+      h = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&b), __float2half2_rn(1032.0f)), __half2half2(p.s));
     }
+    out[i] = *reinterpret_cast<uint32_t*>(&h);
   }
-#pragma unroll
-  for (int i = 0; i < P; ++i) out[lane * P + i] = x[i];
+  return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// One warp per (row, KV head).
+// Piece e of a CTA's tokens is piece e % (heads * D/8) of token e / (heads * D/8): a thread's
+// pieces are kRowThreads apart, so one division serves them all.
+struct PieceCursor {
+  int per_token, tok, in, step_tok, step_in;
+  __device__ __forceinline__ PieceCursor(int per) : per_token(per) {
+    tok = int(threadIdx.x) / per;
+    in = int(threadIdx.x) - tok * per;
+    step_tok = kRowThreads / per;
+    step_in = kRowThreads - step_tok * per;
+  }
+  __device__ __forceinline__ void next() {
+    tok += step_tok;
+    in += step_in;
+    if (in >= per_token) {
+      in -= per_token;
+      ++tok;
+    }
+  }
+};
+
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads) paged_write_kernel(PagedView c, PagedRows r, const __half* __restrict__ k,
-                                                                  const __half* __restrict__ v) {
+                                                                  const __half* __restrict__ v, int tokens) {
+  constexpr int CH = D / 8;
+  __shared__ TokenPlace s_at[kRowTokens];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long n = (long long)r.n_rows * c.n_kv_heads;
-  for (long long w = ((long long)blockIdx.x * kRowThreads + threadIdx.x) >> 5; w < n;
-       w += (long long)gridDim.x * (kRowThreads / 32)) {
-    const int row = int(w / c.n_kv_heads), head = int(w % c.n_kv_heads);
-    int page, place;
-    bool padding;
-    if (!find_row(c, r, row, lane, &page, &place, &padding)) continue;
-    const int at = row_in_page(c, head, place);
-    const int64_t src = row * r.row_stride + head * D;
-    store_row<FMT, D>(k + src, c.k, c.ks, page * c.page_stride, page * c.scale_stride, at, lane);
-    store_row<FMT, D>(v + src, c.v, c.vs, page * c.page_stride, page * c.scale_stride, at, lane);
-  }
+  const int t0 = blockIdx.x * tokens, n = min(tokens, r.n_rows - t0);
+  PieceCursor p(c.n_kv_heads * CH);
+  // bytes from a head's rows (scales) of a page to the next one's
+  const int head_rows = page_row_bytes_c<FMT>(D) << c.page_shift, head_scales = page_scale_bytes_c<FMT>(D) << c.page_shift;
+  bool found = false;
+  do {  // (the same trips in every thread: all take part in the shuffles)
+    // the rows come while the CTA finds their places
+    uint4 x[kRowBatch], y[kRowBatch];
+    PieceCursor q = p;
+#pragma unroll
+    for (int i = 0; i < kRowBatch; ++i) {
+      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      if (q.tok < n) {
+        const int64_t off = (t0 + q.tok) * r.row_stride + q.in * 8;
+        x[i] = *reinterpret_cast<const uint4*>(k + off);
+        y[i] = *reinterpret_cast<const uint4*>(v + off);
+      }
+      q.next();
+    }
+    if (!found) find_tokens<FMT, D>(c, r, t0, n, s_at);
+    found = true;
+#pragma unroll
+    for (int i = 0; i < kRowBatch; ++i) {
+      TokenPlace at{-1, 0};
+      if (p.tok < n) at = s_at[p.tok];
+      const bool ok = at.rows >= 0;
+      const int head = p.in / CH, ch = p.in % CH;
+      const int64_t row = at.rows + head * head_rows, scale = at.scales + head * head_scales;
+      store_piece<FMT, D>(x[i], c.k + row, c.ks + scale, ch, ok);
+      store_piece<FMT, D>(y[i], c.v + row, c.vs + scale, ch, ok);
+      p.next();
+    }
+  } while (__syncthreads_or(p.tok < n));
 }
 
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(PagedView c, PagedRows r, __half* __restrict__ k,
-                                                                 __half* __restrict__ v) {
+                                                                 __half* __restrict__ v, int tokens) {
+  constexpr int CH = D / 8;
+  __shared__ TokenPlace s_at[kRowTokens];
   pdl_launch_dependents();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const long long n = (long long)r.n_rows * c.n_kv_heads;
-  for (long long w = ((long long)blockIdx.x * kRowThreads + threadIdx.x) >> 5; w < n;
-       w += (long long)gridDim.x * (kRowThreads / 32)) {
-    const int row = int(w / c.n_kv_heads), head = int(w % c.n_kv_heads);
-    int page, place;
-    bool padding;
-    const bool found = find_row(c, r, row, lane, &page, &place, &padding);
-    if (padding) continue;
-    const int64_t dst = row * r.row_stride + head * D;
-    if (!found) {
-      for (int i = 0; i < D / 32; ++i) {
-        if (k) k[dst + lane * (D / 32) + i] = __half(0.0f);
-        if (v) v[dst + lane * (D / 32) + i] = __half(0.0f);
+  const int t0 = blockIdx.x * tokens, n = min(tokens, r.n_rows - t0);
+  find_tokens<FMT, D>(c, r, t0, n, s_at);
+  PieceCursor p(c.n_kv_heads * CH);
+  // bytes from a head's rows (scales) of a page to the next one's
+  const int head_rows = page_row_bytes_c<FMT>(D) << c.page_shift, head_scales = page_scale_bytes_c<FMT>(D) << c.page_shift;
+  while (p.tok < n) {
+    StoredPiece<FMT> x[kRowBatch], y[kRowBatch];
+    PieceCursor q = p;
+#pragma unroll
+    for (int i = 0; i < kRowBatch; ++i) {
+      x[i] = y[i] = StoredPiece<FMT>{};
+      if (q.tok < n) {
+        const TokenPlace at = s_at[q.tok];
+        if (at.rows >= 0) {
+          const int head = q.in / CH, ch = q.in % CH;
+          const int64_t row = at.rows + head * head_rows, scale = at.scales + head * head_scales;
+          if (k) x[i] = load_piece<FMT>(c.k + row, c.ks + scale, ch);
+          if (v) y[i] = load_piece<FMT>(c.v + row, c.vs + scale, ch);
+        }
       }
-      continue;
+      q.next();
     }
-    const int at = row_in_page(c, head, place);
-    if (k) load_row<FMT, D>(k + dst, c.k, c.ks, page * c.page_stride, page * c.scale_stride, at, lane);
-    if (v) load_row<FMT, D>(v + dst, c.v, c.vs, page * c.page_stride, page * c.scale_stride, at, lane);
+#pragma unroll
+    for (int i = 0; i < kRowBatch; ++i) {
+      const int64_t at = p.tok < n ? s_at[p.tok].rows : -2;
+      if (at != -2) {  // (padding rows stay as they are)
+        const int64_t off = (t0 + p.tok) * r.row_stride + p.in * 8;
+        const uint4 zero = make_uint4(0, 0, 0, 0);
+        if (k) *reinterpret_cast<uint4*>(k + off) = at < 0 ? zero : values_of<FMT>(x[i], p.in % CH);
+        if (v) *reinterpret_cast<uint4*>(v + off) = at < 0 ? zero : values_of<FMT>(y[i], p.in % CH);
+      }
+      p.next();
+    }
   }
 }
 
-int row_grid(const PagedView& c, const PagedRows& r, int n_sms) {
-  const long long warps = (long long)r.n_rows * c.n_kv_heads;
-  const long long ctas = (warps + kRowThreads / 32 - 1) / (kRowThreads / 32);
-  return int(ctas < n_sms * 8LL ? ctas : n_sms * 8LL);
+// Tokens a CTA takes: few enough to give every SM a few CTAs, and no more than two batches of
+// pieces a thread: finding places costs two rounds of loads, which the other CTAs hide.
+int row_tokens(const PagedView& c, const PagedRows& r, int n_sms) {
+  const int spread = (r.n_rows + 4 * n_sms - 1) / (4 * n_sms);
+  const int full = 2 * kRowBatch * kRowThreads / (c.n_kv_heads * (c.head_dim / 8));
+  const int most = full < kRowTokens ? full : kRowTokens;
+  const int t = spread < most ? spread : most;
+  return t < 1 ? 1 : t;
 }
 
 }  // namespace
 
 cudaError_t launch_paged_write(const PagedView& c, int format, const PagedRows& r, const void* k, const void* v,
                                int n_sms, cudaStream_t s) {
-  const dim3 grid(row_grid(c, r, n_sms)), block(kRowThreads);
+  const int tokens = row_tokens(c, r, n_sms);
+  const dim3 grid((r.n_rows + tokens - 1) / tokens), block(kRowThreads);
 #define QSA_WRITE(F, D)                                                                                      \
   if (format == F && c.head_dim == D)                                                                        \
-    return launch_pdl(paged_write_kernel<F, D>, grid, block, 0, s, 1, c, r, (const __half*)k, (const __half*)v)
+    return launch_pdl(paged_write_kernel<F, D>, grid, block, 0, s, 1, c, r, (const __half*)k, (const __half*)v, tokens)
   QSA_WRITE(QSA_PAGE_F16, 64);
   QSA_WRITE(QSA_PAGE_F16, 128);
   QSA_WRITE(QSA_PAGE_FP8, 64);
@@ -195,10 +319,11 @@ cudaError_t launch_paged_write(const PagedView& c, int format, const PagedRows& 
 
 cudaError_t launch_paged_read(const PagedView& c, int format, const PagedRows& r, void* k, void* v, int n_sms,
                               cudaStream_t s) {
-  const dim3 grid(row_grid(c, r, n_sms)), block(kRowThreads);
+  const int tokens = row_tokens(c, r, n_sms);
+  const dim3 grid((r.n_rows + tokens - 1) / tokens), block(kRowThreads);
 #define QSA_READ(F, D)                                                                            \
   if (format == F && c.head_dim == D)                                                             \
-    return launch_pdl(paged_read_kernel<F, D>, grid, block, 0, s, 1, c, r, (__half*)k, (__half*)v)
+    return launch_pdl(paged_read_kernel<F, D>, grid, block, 0, s, 1, c, r, (__half*)k, (__half*)v, tokens)
   QSA_READ(QSA_PAGE_F16, 64);
   QSA_READ(QSA_PAGE_F16, 128);
   QSA_READ(QSA_PAGE_FP8, 64);
