@@ -78,7 +78,9 @@ struct PaCfg {
   static_assert(KB % 1024 == 0, "swizzled tiles start on their pattern's border");
 };
 
-// What merge CTA i joins: the segment that team i is the first to continue.
+// What merge CTA i joins: if the batch has no more segments than teams, segment i (written by
+// the team that ends it, or by the first one that continues it), else the segment that team i is
+// the first to continue.
 struct PaSplit {
   int seq, head;    // seq < 0: nothing
   int first, last;  // teams that hold a part
@@ -450,6 +452,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_TEAM));
   const int g = lane >> 2, t = lane & 3;
   const float c1 = a.sm_scale * 1.44269504088896341f;  // logits in units of log 2
+  const bool by_segment = (long long)a.n_seqs * Hkv <= n_teams;
   if (tid == 0) {
     // the first team that continues a segment names the parts to merge
     PaSplit sp;
@@ -466,7 +469,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         sp.slot0 = 2 * (cta - 1) + (before < b);
       }
     }
-    splits[cta] = sp;
+    if (!by_segment) splits[cta] = sp;
+    else if (sp.seq >= 0) splits[sp.seq * Hkv + sp.head] = sp;
   }
   // bad lengths and the results of sequences without cells: a team looks after its share
   for (int s = cta; s < a.n_seqs; s += n_teams) {
@@ -475,6 +479,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     if (tid == 0 && n > table_cells) record_status(a.status, QSA_ERR_CAPACITY);
     if (n <= 0) {
       const int rows = T * a.n_q_heads;
+      if (by_segment)
+        for (int h = tid; h < Hkv; h += kPaThreads) splits[s * Hkv + h].seq = -1;
       for (int e = tid; e < rows * D; e += kPaThreads) a.out[(int64_t)s * rows * D + e] = 0.0f;
       if (a.lse)
         for (int e = tid; e < rows; e += kPaThreads) a.lse[(int64_t)s * rows + e] = -INFINITY;
@@ -843,6 +849,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     const bool complete = tile0 == 0 && tile1 == cur.nt;
     float* const out_part = part + int64_t(2 * cta + (first_segment ? 0 : 1)) * R * (D + 4);
     const int64_t out_row = int64_t(cur.seq) * T * a.n_q_heads + cur.head * G;
+    if (complete && by_segment && tid == 0) splits[cur.seq * Hkv + cur.head].seq = -1;
     if (tid < R) {
       // a warp that saw nothing has l = 0 (a NaN logit makes l, and then everything, NaN)
       float M = -INFINITY, L = 0.0f;
@@ -915,83 +922,81 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   }
 }
 
-// CTA (i, row): joins row `row` of the parts of the segment that team i was the first to
-// continue. Each warp takes every fourth part, a lane 4 (2) dims of it, so that all its
-// loads are in flight at once; the weights come from the lanes that loaded the statistics.
-constexpr int kPmThreads = 128;
-constexpr int kPmWarps = kPmThreads / 32;
+// Joins the parts of the segments that were cut: CTA x those of splits[x], its warps one row each
+// or, with many parts, 2 to 8 warps a row, every one with several parts in flight; gridDim.y
+// CTAs share a segment's rows.
+constexpr int kPmWarps = 8;
+constexpr int kPmBatch = 14;
 
 template <int D>
-__global__ void __launch_bounds__(kPmThreads) paged_merge_kernel(PagedAttendArgs a, const float* __restrict__ part,
-                                                                 const PaSplit* __restrict__ splits, int n_kv_heads) {
+__global__ void __launch_bounds__(32 * kPmWarps) paged_merge_kernel(PagedAttendArgs a, const float* __restrict__ part,
+                                                                    const PaSplit* __restrict__ splits, int n_kv_heads) {
   constexpr int V = D / 32;
-  __shared__ float s_o[kPmWarps][D];
-  __shared__ float s_w[kPaMaxTeams];
-  __shared__ float s_ml[kPmWarps][2];
+  __shared__ float s_o[kPmWarps][D], s_ml[kPmWarps][2];
   pdl_launch_dependents();
   pdl_wait();
   const PaSplit sp = splits[blockIdx.x];
   if (sp.seq < 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int G = a.n_q_heads / n_kv_heads, T = a.n_queries, R = G * T, col = blockIdx.y;
+  const int G = a.n_q_heads / n_kv_heads, T = a.n_queries, R = G * T;
   const int n = sp.last - sp.first + 1;
+  const int ways = n <= kPmBatch ? 1 : n <= 2 * kPmBatch ? 2 : n <= 4 * kPmBatch ? 4 : 8;  // warps a row
+  const int way = warp % ways, rows = kPmWarps / ways;
   const int64_t step = int64_t(R) * (D + 4);
-  const auto row_of = [&](int p) { return part + (p == 0 ? sp.slot0 : 2 * (sp.first + p)) * step + col * (D + 4); };
-  // weights of all parts
-  float M = -INFINITY;
-  for (int p = threadIdx.x; p < n; p += kPmThreads) M = fmaxf(M, row_of(p)[D]);
-  M = warp_max(M);
-  if (lane == 0) s_ml[warp][0] = M;
-  __syncthreads();
+  for (int r0 = blockIdx.y * rows; r0 < R; r0 += gridDim.y * rows) {
+    const int col = r0 + warp / ways;
+    const auto row_of = [&](int p) { return part + (p == 0 ? sp.slot0 : 2 * (sp.first + p)) * step + col * (D + 4); };
+    float M = -INFINITY, L = 0.0f, o[V];
 #pragma unroll
-  for (int w = 0; w < kPmWarps; ++w) M = fmaxf(M, s_ml[w][0]);
-  float L = 0.0f;
-  for (int p = threadIdx.x; p < n; p += kPmThreads) {
-    const float l = row_of(p)[D + 1], w = l == 0.0f ? 0.0f : ex2(row_of(p)[D] - M);
-    s_w[p] = w;
-    L += w * l;
-  }
-  L = warp_sum(L);
-  if (lane == 0) s_ml[warp][1] = L;
-  __syncthreads();
-  L = 0.0f;
+    for (int i = 0; i < V; ++i) o[i] = 0.0f;
+    // adds m, l, x (a part that saw nothing has l = 0)
+    const auto add = [&](float m, float l, const float* x) {
+      if (l == 0.0f) return;
+      const float to = fmaxf(M, m), keep = M == to ? 1.0f : ex2(M - to), w = m == to ? 1.0f : ex2(m - to);
+      M = to;
+      L = L * keep + w * l;
 #pragma unroll
-  for (int w = 0; w < kPmWarps; ++w) L += s_ml[w][1];
-  float o[V];
+      for (int i = 0; i < V; ++i) o[i] = o[i] * keep + w * x[i];
+    };
+    for (int p0 = way; col < R && p0 < n; p0 += ways * kPmBatch) {
+      float x[kPmBatch][V];
+      float2 ml[kPmBatch];
 #pragma unroll
-  for (int i = 0; i < V; ++i) o[i] = 0.0f;
-  constexpr int B = 10;  // parts in flight
-  for (int p0 = warp; p0 < n; p0 += kPmWarps * B) {
-    float x[B][V];
-#pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int p = p0 + b * kPmWarps;
-#pragma unroll
-      for (int i = 0; i < V; ++i) x[b][i] = 0.0f;
-      if (p < n) {
-        if constexpr (V == 4) *reinterpret_cast<float4*>(x[b]) = reinterpret_cast<const float4*>(row_of(p))[lane];
-        else *reinterpret_cast<float2*>(x[b]) = reinterpret_cast<const float2*>(row_of(p))[lane];
+      for (int b = 0; b < kPmBatch; ++b) {
+        const int p = p0 + b * ways;
+        ml[b] = make_float2(0.0f, 0.0f);
+        if (p < n) {
+          const float* const from = row_of(p);
+          if constexpr (V == 4) *reinterpret_cast<float4*>(x[b]) = reinterpret_cast<const float4*>(from)[lane];
+          else *reinterpret_cast<float2*>(x[b]) = reinterpret_cast<const float2*>(from)[lane];
+          ml[b] = *reinterpret_cast<const float2*>(from + D);
+        }
       }
+#pragma unroll
+      for (int b = 0; b < kPmBatch; ++b) add(ml[b].x, ml[b].y, x[b]);
     }
+    if (ways > 1) {  // (the same in the whole CTA)
 #pragma unroll
-    for (int b = 0; b < B; ++b) {
-      const int p = p0 + b * kPmWarps;
-      const float w = p < n ? s_w[p] : 0.0f;
+      for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
+      if (lane == 0) {
+        s_ml[warp][0] = M;
+        s_ml[warp][1] = L;
+      }
+      __syncthreads();
+      if (way == 0)
+        for (int w = 1; w < ways; ++w) add(s_ml[warp + w][0], s_ml[warp + w][1], &s_o[warp + w][lane * V]);
+      __syncthreads();
+    }
+    if (way == 0 && col < R) {
+      const int64_t row = (int64_t(sp.seq) * T + col / G) * a.n_q_heads + sp.head * G + col % G;
 #pragma unroll
-      for (int i = 0; i < V; ++i) o[i] += w * x[b][i];
+      for (int i = 0; i < V; ++i) o[i] = L == 0.0f ? 0.0f : o[i] / L;
+      float* const to = a.out + row * D + lane * V;
+      if constexpr (V == 4) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(o);
+      else *reinterpret_cast<float2*>(to) = *reinterpret_cast<const float2*>(o);
+      if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
     }
   }
-#pragma unroll
-  for (int i = 0; i < V; ++i) s_o[warp][lane * V + i] = o[i];
-  __syncthreads();
-  const int64_t row = (int64_t(sp.seq) * T + col / G) * a.n_q_heads + sp.head * G + col % G;
-  if (threadIdx.x < D) {
-    float sum = 0.0f;
-#pragma unroll
-    for (int w = 0; w < kPmWarps; ++w) sum += s_o[w][threadIdx.x];
-    a.out[row * D + threadIdx.x] = L == 0.0f ? 0.0f : sum / L;
-  }
-  if (a.lse && threadIdx.x == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
 }
 
 int paged_ctas(int n_sms, int teams) { return min(n_sms, kPaMaxTeams / teams); }
@@ -1058,7 +1063,10 @@ cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, i
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align256(n * sizeof(PaSplit)));
   e = launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::BYTES, s, 1, kmap, vmap, c, a, part, splits);
   if (e != cudaSuccess) return e;
-  return launch_pdl(paged_merge_kernel<D>, dim3(n, R), dim3(kPmThreads), 0, s, 1, a, (const float*)part,
+  // one merge CTA for each segment that may be cut, or several where they are few
+  const long long segments = (long long)a.n_seqs * c.n_kv_heads;
+  const int x = segments < n ? int(segments) : n, y = min(R, max(1, 2 * n_sms / x));
+  return launch_pdl(paged_merge_kernel<D>, dim3(x, y), dim3(32 * kPmWarps), 0, s, 1, a, (const float*)part,
                     (const PaSplit*)splits, c.n_kv_heads);
 }
 
