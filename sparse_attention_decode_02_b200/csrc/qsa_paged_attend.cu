@@ -4,9 +4,9 @@
 // attention reads the whole context for every token, which is what the sparse path avoids.
 //   out = sum_c softmax_c(scale * q.K_c) V_c over the cells c < len - T + u + 1 of query u < T.
 // One pass over K and V with a running maximum and sum, split over the whole batch:
-//  - The (sequence, KV head) segments of a batch, cut into tiles of cells, form one list; team i
-//    of N takes the i-th N-th of it (found from seq_lens on the device), so ragged batches
-//    and single long sequences load every SM alike. A segment cut by a border is written
+//  - The (sequence, KV head) segments of a batch, cut into tiles of cells (a segment's start
+//    counts as two more), form one list; team i of N takes the i-th N-th of it (found from
+//    seq_lens on the device), so ragged batches and single long sequences load every SM alike. A segment cut by a border is written
 //    as partials (m, l, o), at most two a team, which paged_merge_kernel joins:
 //    sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Whole segments are written directly.
 //  - One CTA an SM: two or three teams of four warps, each with its own share of the list, and
@@ -44,6 +44,7 @@ constexpr int kPaWarps = 4;                  // of a team
 constexpr int kPaThreads = 32 * kPaWarps;
 constexpr int kPaTile = 16 * kPaWarps;       // cells of a tile, 16 a warp
 constexpr int kPaMaxTeams = 1024;            // over the GPU
+constexpr int kPaStart = 2;                  // a segment's start (queries, joining) costs about as much as two tiles
 // The running maximum is renewed when a logit passes it by 8 (in log 2), so that weights are
 // at most 2^8; times 2^7 they fill f16's range (below 2^16).
 constexpr float kPaSlack = 8.0f;
@@ -213,9 +214,12 @@ __device__ __forceinline__ float v_value(const char* row, const char* scales, in
   }
 }
 
-// Position in the list of tiles: sequence s has ceil(len / 64) tiles for each KV head.
+// Position in the list: sequence s has, for each KV head, kPaStart places for the segment's
+// start and then its nt = ceil(len / 64) tiles. `left` places of the team's share are left,
+// this tile among them.
 struct PaCursor {
   int seq, head, tile, nt, len;
+  long long left;
 };
 
 // Sum over the CTA in thread order: this thread's exclusive prefix, the total in *total.
@@ -290,7 +294,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     sm100::tma_prefetch_desc(&vmap);
 #pragma unroll
     for (int i = 0; i < STAGES; ++i) {
-      sm100::mbar_init(&sm.full[i], 1);
+      sm100::mbar_init(&sm.full[i], SROW > 0 ? 33 : 1);  // (each lane's copies of scales)
       sm100::mbar_init(&sm.empty[i], kPaWarps);
     }
     sm100::fence_mbar_init();
@@ -301,18 +305,21 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     sm.out_off[tid] = int64_t(u) * a.n_q_heads + h;
     sm.sees[tid] = tid < R ? u : -(1 << 30);
   }
-  pdl_wait();
-  pdl_launch_dependents();
+  pdl_wait();  // (the merge launches when this grid ends: its CTAs find no room beside these)
 
   const auto length = [&](int s) {
     const int n = a.seq_lens[s];
     return n < 0 ? 0 : n > table_cells ? int(table_cells) : n;
   };
-  const auto tiles = [&](int s) { return int(((long long)length(s) + kPaTile - 1) / kPaTile); };
+  const auto tiles = [&](int len) { return int(((long long)len + kPaTile - 1) / kPaTile); };
+  const auto places = [&](int s) {
+    const int len = length(s);
+    return len > 0 ? tiles(len) + kPaStart : 0;
+  };
 
-  // ---- the team's part of the list: tiles [lo, hi) ----
+  // ---- the team's share of the list: places [lo, hi) ----
   long long total = 0, per = 0;
-  int N = 0, extra = 0;  // teams with work: at least one tile each
+  int N = 0, extra = 0;  // teams with a share: at least one place each
   const auto share = [&] {
     total *= Hkv;
     N = int(min((long long)n_teams, total));
@@ -333,7 +340,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
   };
   if (a.n_seqs <= ALL) {
-    const int mine = int(threadIdx.x) < a.n_seqs ? tiles(threadIdx.x) : 0;
+    const int mine = int(threadIdx.x) < a.n_seqs ? places(threadIdx.x) : 0;
     const long long at = cta_scan<ALL / 32>(mine, s_scan, &total) * Hkv;
     share();
     find(threadIdx.x, mine, at);
@@ -341,12 +348,12 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     long long sum, before = 0;
     for (int b = 0; b < a.n_seqs; b += ALL) {
       const int s = b + threadIdx.x;
-      cta_scan<ALL / 32>(s < a.n_seqs ? tiles(s) : 0, s_scan, &sum);
+      cta_scan<ALL / 32>(s < a.n_seqs ? places(s) : 0, s_scan, &sum);
       total += sum;
     }
     share();
     for (int b = 0; b < a.n_seqs; b += ALL) {
-      const int s = b + threadIdx.x, mine = s < a.n_seqs ? tiles(s) : 0;
+      const int s = b + threadIdx.x, mine = s < a.n_seqs ? places(s) : 0;
       const long long at = (before + cta_scan<ALL / 32>(mine, s_scan, &sum)) * Hkv;
       find(s, mine, at);
       before += sum;
@@ -356,22 +363,35 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   __syncthreads();
   PaCursor cur;
   cur.seq = cur.head = cur.tile = cur.nt = cur.len = 0;
+  cur.left = hi - lo;
+  long long b0 = 0;  // where the segment that `lo` is in begins
+  const auto start_segment = [&](PaCursor& p) {
+    p.len = length(p.seq);
+    p.nt = tiles(p.len);
+  };
   if (lo < hi) {
     cur.seq = sm.seq;
-    cur.len = length(cur.seq);
-    cur.nt = tiles(cur.seq);
+    start_segment(cur);
     const long long in = lo - sm.base;
-    cur.head = in >> 31 ? int(in / cur.nt) : int(unsigned(in) / unsigned(cur.nt));
-    cur.tile = int(in - (long long)cur.head * cur.nt);
+    const int all = cur.nt + kPaStart;
+    cur.head = in >> 31 ? int(in / all) : int(unsigned(in) / unsigned(all));
+    const int at = int(in - (long long)cur.head * all);
+    b0 = lo - at;
+    cur.tile = max(0, at - kPaStart);
+    cur.left -= max(0, kPaStart - at);
   }
-  const auto advance = [&](PaCursor& p) {  // to the next tile of the list (which has one)
-    if (++p.tile < p.nt) return;
+  const auto next_segment = [&](PaCursor& p) {  // (the list has one if left stays above 0)
     p.tile = 0;
-    if (++p.head < Hkv) return;
+    p.left -= kPaStart;
+    if (p.left <= 0 || ++p.head < Hkv) return;
     p.head = 0;
-    do p.len = length(++p.seq);
-    while (p.len == 0);
-    p.nt = tiles(p.seq);
+    do ++p.seq;
+    while (length(p.seq) == 0);
+    start_segment(p);
+  };
+  const auto next_tile = [&](PaCursor& p) {
+    --p.left;
+    if (++p.tile == p.nt && p.left > 0) next_segment(p);
   };
 
   // =============================== loading warps ===============================
@@ -389,20 +409,20 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // the pages of two tiles ahead are on their way
     PaCursor ld = cur;
     int page = 0, page1 = 0;
-    if (lo < hi) page = entry(ld);
-    if (lo + 1 < hi) {
-      advance(cur);
-      page1 = entry(cur);
+    if (ld.left > 0) {
+      page = entry(ld);
+      next_tile(cur);
+      if (cur.left > 0) page1 = entry(cur);
     }
     int slot = 0;
     uint32_t parity = 1;
 #pragma unroll 1
-    for (long long at = lo; at < hi; ++at) {
+    while (ld.left > 0) {
       const PaCursor next = cur;
       int page2 = 0;
-      if (at + 2 < hi) {
-        advance(cur);
-        page2 = entry(cur);
+      if (cur.left > 0) {
+        next_tile(cur);
+        if (cur.left > 0) page2 = entry(cur);
       }
       if (!sm100::mbar_wait(&sm.empty[slot], parity)) {
         if (lane == 0) record_status(a.status, QSA_ERR_TIMEOUT);
@@ -418,7 +438,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         if (lost) record_status(a.status, QSA_ERR_BAD_INDEX);
         sm.lost[slot] = lost;
         if (n_loads == 0) sm100::mbar_arrive(bar);
-        else sm100::mbar_arrive_expect_tx(bar, n_loads * rows * 2 * (ROW + SROW));
+        else sm100::mbar_arrive_expect_tx(bar, n_loads * rows * 2 * ROW);
       }
       __syncwarp();
       if (ok && leads) {
@@ -430,12 +450,22 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           sm100::tma_load_3d(dst + x * kPaTile * 128, &kmap, x * 64, row * LINE / 128, page, bar);
           sm100::tma_load_3d(dst + C::KB + x * kPaTile * 128, &vmap, x * 64, row * LINE / 128, page, bar);
         }
-        if constexpr (SROW > 0) {
-          const uint32_t sdst = sring + slot * 2 * C::SB + lane * 16 * SROW;
-          const int64_t off = page * c.scale_stride + (int64_t)row * SROW;
-          sm100::bulk_load(sdst, c.ks + off, rows * SROW, bar);
-          sm100::bulk_load(sdst + C::SB, c.vs + off, rows * SROW, bar);
+      }
+      if constexpr (SROW > 0) {
+        // scales in 16-byte pieces, one or two a lane (they are too small for bulk copies: 64 bytes a page)
+        const unsigned there = __ballot_sync(0xffffffffu, ok);
+#pragma unroll
+        for (int i = 0; i < SROW / 4; ++i) {
+          const int piece = i * 32 + lane, of_v = piece / (4 * SROW), in = piece % (4 * SROW), cells = in / SROW;
+          const int at = __shfl_sync(0xffffffffu, page, cells);
+          if ((there >> cells) & 1) {
+            const int first = (ld.tile * kPaTile + cells * 16) & ((1 << c.page_shift) - 1);
+            const char* const src = (of_v ? c.vs : c.ks) + at * c.scale_stride +
+                                    (int64_t)row_in_page(c, ld.head, first) * SROW + in % SROW * 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(sring + (slot * 2 + of_v) * C::SB + in * 16), "l"(src) : "memory");
+          }
         }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sm100::smem_u32(bar)) : "memory");
       }
       ld = next;
       page = page1;
@@ -457,16 +487,15 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // the first team that continues a segment names the parts to merge
     PaSplit sp;
     sp.seq = -1;
-    if (lo < hi && cur.tile > 0) {
-      const long long b = lo - cur.tile, e = b + cur.nt;
-      const long long before = start_of(cta - 1);
-      if (before <= b) {
-        const long long border = extra * (per + 1), last = e - 1;
+    if (cur.left > 0 && cur.tile > 0) {
+      const long long before = start_of(cta - 1), last = b0 + kPaStart + cur.nt - 1;
+      if (before <= b0 + kPaStart) {  // the team before this one has the segment's first tile
+        const long long border = extra * (per + 1);
         sp.seq = cur.seq;
         sp.head = cur.head;
         sp.first = cta - 1;
         sp.last = int(last < border ? last / (per + 1) : extra + (last - border) / per);
-        sp.slot0 = 2 * (cta - 1) + (before < b);
+        sp.slot0 = 2 * (cta - 1) + (before < b0);
       }
     }
     if (!by_segment) splits[cta] = sp;
@@ -494,8 +523,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   uint32_t parity = 0;
   bool timed_out = false;
   bool first_segment = true;
-  for (long long at = lo; at < hi;) {
-    const int tile0 = cur.tile, tile1 = int(min((long long)cur.nt, tile0 + (hi - at)));
+  while (cur.left > 0) {
+    const int tile0 = cur.tile, tile1 = int(min((long long)cur.nt, tile0 + cur.left));
     const int len = cur.len, seen = len - T + 1;  // cells before `seen` are seen by every query
 
     // queries: B fragments, column = (query, head) row of this KV head
@@ -914,11 +943,9 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
     sm100::named_bar_sync(1 + team, kPaThreads);  // sm.m, sm.l, s_join and s_q are free
 
-    // ---- next segment ----
-    at += tile1 - tile0;
     first_segment = false;
-    cur.tile = tile1 - 1;
-    if (at < hi) advance(cur);
+    cur.left -= tile1 - tile0;
+    if (cur.left > 0) next_segment(cur);
   }
 }
 
