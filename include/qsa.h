@@ -348,7 +348,8 @@ qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, 
  * Probabilities are finite and not negative (weights that are NaN count as 0); they need
  * not sum to 1. status (may be NULL) is a device i32 that gets QSA_ERR_BAD_INDEX, if it was
  * 0, where something is reported. Pointers are aligned to their elements. Needs no context;
- * nothing is written but the outputs and status. 0 <= n_seqs, 0 <= max_drafts <= 64. */
+ * nothing is written but the outputs and status. 0 <= n_seqs, 0 <= max_drafts <= 64,
+ * 1 <= vocab <= 2^30. */
 #define QSA_MAX_DRAFTS 64
 qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, const float* draft_probs,
                              int64_t draft_stride, const int32_t* draft_tokens, const int32_t* n_drafts,
@@ -444,10 +445,10 @@ size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, i
  *   lse [n_seqs][n_queries][n_q_heads] f32 or NULL: log sum_c exp(sm_scale * q_i . K[c][g]),
  *     which qsa_cp_merge takes to join parts of a sequence held on several devices.
  * A query that sees no cell (seq_lens[s] = 0, or fewer tokens than queries) gives out = 0
- * and lse = -inf. sm_scale 0 means 1/sqrt(head_dim). f32 softmax and accumulation; values of
+ * and lse = -inf. sm_scale 0 means 1/sqrt(head_dim); at most 1e20. f32 softmax and accumulation; values of
  * cells that a query does not see (whatever they hold) do not change its result, and the
  * result of a sequence does not depend on the others of the batch beyond f32 rounding.
- * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8. Cells of a page id outside the pool
+ * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8, n_seqs up to 65,536. Cells of a page id outside the pool
  * are skipped (QSA_ERR_BAD_INDEX); a length beyond the table counts as the table's
  * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). */
 qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_stride, int32_t n_queries,

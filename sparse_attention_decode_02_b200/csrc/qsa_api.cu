@@ -575,7 +575,7 @@ qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, c
                              const float* uniforms, int32_t n_seqs, int32_t max_drafts, int32_t vocab,
                              int32_t* n_accepted, int32_t* next_token, int32_t* status, qsa_stream_t stream) {
   if (n_seqs < 0 || max_drafts < 0 || vocab < 1) return QSA_ERR_INVALID_ARG;
-  if (max_drafts > QSA_MAX_DRAFTS) return QSA_ERR_UNSUPPORTED;
+  if (max_drafts > QSA_MAX_DRAFTS || vocab > (1 << 30)) return QSA_ERR_UNSUPPORTED;
   if (target_stride == 0) target_stride = vocab;
   if (draft_stride == 0) draft_stride = vocab;
   if (target_stride < vocab || draft_stride < vocab) return QSA_ERR_INVALID_ARG;
@@ -657,7 +657,7 @@ qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_
   const int64_t row = int64_t(n_q_heads) * cache->head_dim;
   if (q_stride == 0) q_stride = row;
   if (q_stride < row || q_stride % 8 || n_seqs < 0 || table_width < 0) return QSA_ERR_INVALID_ARG;
-  if (!(sm_scale >= 0.0f) || sm_scale > 1e30f) return QSA_ERR_INVALID_ARG;
+  if (!(sm_scale >= 0.0f) || sm_scale > 1e20f) return QSA_ERR_INVALID_ARG;  // (logits stay finite in f32)
   if (n_seqs == 0) return QSA_OK;
   if (n_seqs > 65536) return QSA_ERR_UNSUPPORTED;
   if (table_width < 1 || !usable(q, 16) || !usable(block_table, 4) || !usable(seq_lens, 4) || !usable(out, 16) ||

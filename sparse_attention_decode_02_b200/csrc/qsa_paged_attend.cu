@@ -57,9 +57,11 @@ struct PaCfg {
   static constexpr int KB = kPaTile * ROW;                 // bytes of a tile's K (V) rows
   static constexpr int SB = kPaTile * SROW;                // and of their scales
   static constexpr int KS = D / 16;                        // MMA k-steps of q.K = m-tiles of P.V
-  // Teams of a CTA (one CTA an SM): three with one column group, two where more columns need
-  // the registers or 256-byte rows the shared memory. A fourth resp. third warpgroup loads.
-  static constexpr int TEAMS = NC == 1 && ROW <= 128 ? 3 : 2;
+  // Teams of a CTA (one CTA an SM): three where a thread's sums take up to 64 registers (f16
+  // rows: 32), two where they take more or 256-byte rows need the shared memory. One more
+  // warpgroup loads. (Two column groups of 128 dims: three teams take 116 us against 133 at
+  // 4 bits, 69 against 71 at e4m3; four groups of 64-dim f16 rows 43 against 41.)
+  static constexpr int TEAMS = KS * NC <= (FMT == QSA_PAGE_F16 ? 8 : 16) && ROW <= 128 ? 3 : 2;
   static constexpr int THREADS = kPaThreads * (TEAMS + 1);
   // registers a thread: at launch, and as the warpgroups split them
   static constexpr int REGS = TEAMS == 3 ? 128 : 168;
@@ -287,7 +289,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   const int G = a.n_q_heads / c.n_kv_heads, T = a.n_queries, R = G * T, Hkv = c.n_kv_heads;
   const int n_teams = gridDim.x * TEAMS;
   const int cta = blockIdx.x * TEAMS + team;  // the team's index in the GPU
-  const long long table_cells = (long long)a.table_width << c.page_shift;
+  // (cell numbers stay clear of 2^31)
+  const long long table_cells = min((long long)a.table_width << c.page_shift, 0x7fffff00ll);
 
   if (loads && lane == 0 && warp < TEAMS) {
     sm100::tma_prefetch_desc(&kmap);
@@ -664,6 +667,34 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
         }
 
+        // V's codes are on their way from shared memory during the softmax
+        uint4 vraw[4];
+        __half2 vsc[2];  // 4-bit scales of cells (0, 1) and (2, 3)
+        if constexpr (FMT != QSA_PAGE_F16) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = ((i & 1) ? pv1 : pv0) + (i >> 1) * 8;
+            const uint32_t at_row = uv + swizzled(row * ROW + g * (ROW / 8));
+            if constexpr (ROW == 128) {
+              vraw[i] = lds128(at_row);
+            } else if constexpr (ROW == 64) {
+              const uint2 w = lds64(at_row);
+              vraw[i] = make_uint4(w.x, w.y, 0u, 0u);
+            } else {
+              vraw[i] = make_uint4(lds32(at_row), 0u, 0u, 0u);
+            }
+          }
+          if constexpr (FMT == QSA_PAGE_INT4) {
+            const int grp = D == 128 ? g >> 1 : g >> 2;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const uint32_t x = lds32(uvs + (pv0 + 8 * i) * SROW + (grp >> 1) * 4);
+              const uint32_t y = lds32(uvs + (pv1 + 8 * i) * SROW + (grp >> 1) * 4);
+              vsc[i] = as_h2(__byte_perm(x, y, (grp & 1) ? 0x7632 : 0x5410));
+            }
+          }
+        }
+
         // logits: times the row's scale (e4m3), masked
         float vf[2] = {kPaTop, kPaTop};
         if constexpr (FMT == QSA_PAGE_FP8) {
@@ -757,32 +788,6 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
 
         // O^T += V^T P^T
-        uint4 raw[4];
-        __half2 vsc[2];  // 4-bit scales of cells (0, 1) and (2, 3)
-        if constexpr (FMT != QSA_PAGE_F16) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int row = ((i & 1) ? pv1 : pv0) + (i >> 1) * 8;
-            const uint32_t at_row = uv + swizzled(row * ROW + g * (ROW / 8));
-            if constexpr (ROW == 128) {
-              raw[i] = lds128(at_row);
-            } else if constexpr (ROW == 64) {
-              const uint2 w = lds64(at_row);
-              raw[i] = make_uint4(w.x, w.y, 0u, 0u);
-            } else {
-              raw[i] = make_uint4(lds32(at_row), 0u, 0u, 0u);
-            }
-          }
-          if constexpr (FMT == QSA_PAGE_INT4) {
-            const int grp = D == 128 ? g >> 1 : g >> 2;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const uint32_t x = lds32(uvs + (pv0 + 8 * i) * SROW + (grp >> 1) * 4);
-              const uint32_t y = lds32(uvs + (pv1 + 8 * i) * SROW + (grp >> 1) * 4);
-              vsc[i] = as_h2(__byte_perm(x, y, (grp & 1) ? 0x7632 : 0x5410));
-            }
-          }
-        }
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           float d[NC][4];
@@ -795,12 +800,12 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               if constexpr (FMT == QSA_PAGE_FP8) {
-                const uint32_t z = __byte_perm(word_of(raw[2 * i], k >> 1), word_of(raw[2 * i + 1], k >> 1),
+                const uint32_t z = __byte_perm(word_of(vraw[2 * i], k >> 1), word_of(vraw[2 * i + 1], k >> 1),
                                                (k & 1) ? 0x7362 : 0x5140);
                 f[2 * i] = e4m3x2(z, 0);
                 f[2 * i + 1] = e4m3x2(z, 1);
               } else {
-                const uint32_t x = word_of(raw[2 * i], k >> 2), y = word_of(raw[2 * i + 1], k >> 2);
+                const uint32_t x = word_of(vraw[2 * i], k >> 2), y = word_of(vraw[2 * i + 1], k >> 2);
                 f[2 * i] = int4x2(__byte_perm(x, y, 0x5410), k & 3, vsc[i]);
                 f[2 * i + 1] = int4x2(__byte_perm(x, y, 0x7632), k & 3, vsc[i]);
               }

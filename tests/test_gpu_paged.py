@@ -399,6 +399,51 @@ def test_one_very_long_among_short_sequences():
     p.check(q, *p.attend(q))
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+def test_many_kv_heads(fmt):
+    p = Pool([37, 5, 0, 200], fmt, 24, 64, 16, seed=6)
+    p.append([37, 5, 0, 200])
+    q = _query(p.rng, 4, 3, 24, 64)
+    p.check(q, *p.attend(q))
+
+
+@pytest.mark.parametrize("hq,hkv,dim,T", [(32, 4, 128, 1), (32, 4, 128, 4), (8, 1, 64, 2)])
+def test_more_segments_than_teams_and_fewer(hq, hkv, dim, T):
+    """Batches around the number of work shares of the GPU, whose borders then fall on segments'
+    starts, ends and single tiles."""
+    for S, top in ((1, 64 * 500), (3, 64 * 120), (74, 300), (111, 130), (148, 64), (300, 200)):
+        lens = [top - i % min(top, 129) for i in range(S)]
+        p = Pool(lens, "int4", hkv, dim, 128, seed=S)
+        p.append(lens)
+        q = _query(p.rng, S, T, hq, dim)
+        out, lse = p.attend(q)
+        keep = sorted({0, S // 3, S // 2, S - 1})
+        for i in keep:
+            k, v = p.values(i)
+            assert_attention(out[i].cpu().numpy().astype(np.float64), lse[i].cpu().numpy().astype(np.float64), q[i], k, v,
+                             what=f"{i} of {S}")
+        # the others against the same cache one at a time
+        ws = torch.empty(p.cache.workspace_bytes(hq, T), dtype=torch.uint8, device="cuda")
+        one, one_lse = torch.empty(1, T, hq, dim, device="cuda"), torch.empty(1, T, hq, device="cuda")
+        for i in range(0, S, 7):
+            p.cache.attend(H.to_dev(q[i:i + 1]), p.table_dev[i:i + 1], _i32(lens[i:i + 1]), one, ws, lse=one_lse)
+            assert torch.allclose(one[0], out[i], rtol=0, atol=2e-5) and torch.allclose(one_lse[0], lse[i], rtol=1e-5, atol=1e-5)
+
+
+def test_sequences_that_share_pages():
+    """Two sequences with a common prefix hold it once."""
+    p = Pool([64, 40], "fp8", 2, 64, 16)
+    p.append([64, 0])
+    p.table[1, :2] = p.table[0, :2]
+    p.table_dev = _i32(p.table)
+    p.lens[1] = 32
+    for rows in p.rows:
+        rows[1] = rows[0][:32].copy()
+    p.append([0, 5])        # goes on in a page of its own
+    q = _query(p.rng, 2, 2, 8, 64)
+    p.check(q, *p.attend(q))
+
+
 def test_pages_past_32_bit_offsets():
     """The last pages of a pool of more than 2^32 bytes (and 2^31 elements)."""
     n, heads, page, dim = 17000, 4, 256, 128        # 262,144 bytes a page: 4.5 GB each for K and V

@@ -63,6 +63,21 @@ def test_equal_to_the_plain_form(V, K, drafter):
     assert int(status) == 0
 
 
+@pytest.mark.parametrize("K", [31, 32, 33, 64])
+def test_long_drafts(K):
+    rng = np.random.default_rng(K)
+    target, draft, tokens, u = _random(rng, 12, K, 500)
+    for i in range(12):         # from none to all accepted
+        u[i, :K] *= 1e-3 if i % 3 == 0 else 1.0
+        u[i, min(i * 6, K - 1)] = 0.999 if i % 2 else 0.0
+    u[0, :K] = u[1, :K] = 0.0   # everything with a probability
+    want = [P.verify(target[i], draft[i], tokens[i], u[i]) for i in range(12)]
+    assert max(m for m, _ in want) == K and min(m for m, _ in want) < 32
+    assert _verify(target, draft, tokens, u) == want
+    want = [P.verify(target[i], None, tokens[i], u[i]) for i in range(12)]
+    assert _verify(target, None, tokens, u) == want
+
+
 def test_large_vocabulary_and_batch():
     rng = np.random.default_rng(1)
     target, draft, tokens, u = _random(rng, 2, 1, 1_000_003)

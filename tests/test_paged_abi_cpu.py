@@ -107,7 +107,7 @@ ATTEND = dict(q=PTR, q_stride=0, n_queries=1, n_q_heads=32, block_table=PTR, tab
     (dict(n_q_heads=30), UNSUPPORTED), (dict(n_q_heads=36), UNSUPPORTED), (dict(table_width=0), INVALID),
     (dict(n_seqs=-1), INVALID), (dict(n_seqs=65537), UNSUPPORTED), (dict(seq_lens=None), INVALID),
     (dict(block_table=PTR + 2), INVALID), (dict(sm_scale=-1.0), INVALID), (dict(sm_scale=float("nan")), INVALID),
-    (dict(sm_scale=float("inf")), INVALID), (dict(out=None), INVALID), (dict(lse=PTR + 2), INVALID),
+    (dict(sm_scale=float("inf")), INVALID), (dict(sm_scale=2e20), INVALID), (dict(out=None), INVALID), (dict(lse=PTR + 2), INVALID),
     (dict(workspace=None), INVALID), (dict(workspace=PTR + 128), INVALID), (dict(status=PTR + 2), INVALID)])
 def test_bad_attend_arguments_are_refused(lib, bad, want):
     assert lib.qsa_paged_attend(ctypes.byref(_cache()), *{**ATTEND, **bad}.values()) == want
@@ -128,7 +128,7 @@ VERIFY = dict(target=PTR, target_stride=0, draft=PTR, draft_stride=0, tokens=PTR
     (dict(target=None), INVALID), (dict(target=PTR + 2), INVALID), (dict(target_stride=99), INVALID),
     (dict(draft_stride=99), INVALID), (dict(draft=PTR + 1), INVALID), (dict(tokens=None), INVALID),
     (dict(uniforms=None), INVALID), (dict(n_seqs=-1), INVALID), (dict(max_drafts=-1), INVALID),
-    (dict(max_drafts=65), UNSUPPORTED), (dict(vocab=0), INVALID), (dict(n_accepted=None), INVALID),
+    (dict(max_drafts=65), UNSUPPORTED), (dict(vocab=0), INVALID), (dict(vocab=2 ** 30 + 1), UNSUPPORTED), (dict(n_accepted=None), INVALID),
     (dict(next_token=PTR + 2), INVALID), (dict(n_drafts=PTR + 2), INVALID), (dict(status=PTR + 2), INVALID)])
 def test_bad_verify_arguments_are_refused(lib, bad, want):
     assert lib.qsa_verify_drafts(*{**VERIFY, **bad}.values()) == want
