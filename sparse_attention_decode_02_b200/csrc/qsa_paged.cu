@@ -9,6 +9,11 @@
 // some tokens: it finds their places once (sequence by a count over row_start, then page), then
 // every thread moves 16-byte pieces of f16 rows, 8 values each, with several K and V pieces
 // in flight; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
+// Measured on B200 (us; share of a copy's 6,568 GB/s): 61,789 tokens x 4 heads x 128 dims
+// written to f16 pages 40 (96%), to e4m3 38 (76%: 70% of the issue slots, the quantising);
+// 126,253 read from e4m3 65 (92%); 73,000 written in 4 bits and read back 76 (61%, issue
+// slots again); 64 tokens 2.9 (latency). Two K and V pieces in flight a thread beat four by 9%
+// (registers: more CTAs an SM), f32 codes rounded by an addition the conversions by a third.
 #include "qsa_paged.cuh"
 
 namespace qsa {

@@ -31,6 +31,13 @@
 //  - Code that runs once a segment is kept short and rolled: instructions come cold from L2
 //    at some 50 cycles each, so an unrolled copy of the tile's code for the segment's end, or
 //    a result loop unrolled over the columns, cost 19 us a segment.
+// Measured on B200 (us; share of a copy's 6,568 GB/s over the bytes that must be read): one
+// sequence of 126,253 tokens in f16 47 (84%), 255,181 in e4m3 53 (78%), 128 sequences of up to
+// 8,192 in e4m3 113 (82%): bound by the loads, less some 5 us to start and 4 us to merge. 24
+// sequences of up to 32,768 with four queries each in 4 bits 216 (16%), with one 88 (40%): bound
+// by the instructions that turn codes into operands and weights into fragments, and their
+// latency at 8 to 12 warps an SM (issue slots 48% busy, tensor pipe 35%). A lone sequence of
+// 1,024 tokens 7.9, all latency.
 #include <atomic>
 
 #include "qsa_paged.cuh"
