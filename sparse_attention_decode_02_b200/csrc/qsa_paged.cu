@@ -6,14 +6,15 @@
 //   e4m3: scale = amax * (1/448), code = e4m3(x * (448 * (1/amax)));
 //   4 bits: per 32 dims s = f16(amax * (1/7)), code = rint(x * (1/s)) in [-7, 7].
 // Both calls only move data: a row's 2 * head_dim f16 bytes and its stored bytes. A CTA takes
-// some tokens: it finds their places once (sequence by a count over row_start, then page), then
-// every thread moves 16-byte pieces of f16 rows, 8 values each, with several K and V pieces
-// in flight; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
+// some tokens: it finds their places once (sequence, then page), then every thread moves pieces
+// of K and V rows; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
 // Measured on B200 (us; share of a copy's 6,568 GB/s): 61,789 tokens x 4 heads x 128 dims
-// written to f16 pages 40 (96%), to e4m3 38 (76%: 70% of the issue slots, the quantising);
-// 126,253 read from e4m3 65 (92%); 73,000 written in 4 bits and read back 76 (61%, issue
-// slots again); 64 tokens 2.9 (latency). Two K and V pieces in flight a thread beat four by 9%
-// (registers: more CTAs an SM), f32 codes rounded by an addition the conversions by a third.
+// written to f16 pages 41 (95%), to e4m3 33 (88%); 126,253 read from e4m3 65 (92%); 73,000
+// written in 4 bits and read back 67 (70%: the issue slots, in both); 64 tokens 2.7 (latency).
+// Pieces of 16 values take fewer instructions a value than 8 (e4m3 writes 38 -> 33, 4-bit
+// 45 -> 35), but a read's stores then leave every other 16 bytes to a second instruction
+// (65 -> 73), so reads take 8. More pieces in flight cost CTAs an SM (registers). Codes are
+// rounded by an addition instead of conversions (4-bit writes a third faster).
 #include "qsa_paged.cuh"
 
 namespace qsa {
@@ -22,7 +23,8 @@ namespace {
 
 constexpr int kRowThreads = 256;
 constexpr int kRowTokens = 64;   // most tokens a CTA takes
-constexpr int kRowBatch = 2;     // K and V pieces a thread has in flight
+constexpr int kRowBatch = 1;     // K and V pieces of 16 values a thread has in flight in a write,
+constexpr int kReadBatch = 2;    // and of 8 in a read
 
 // Where a token's rows are: byte offsets of head 0's row and of its scales; rows -1: nowhere,
 // -2: padding.
@@ -80,41 +82,57 @@ __device__ __forceinline__ void find_tokens(const PagedView& c, const PagedRows&
   __syncthreads();
 }
 
-__device__ __forceinline__ __half2 half2_at(const uint4& x, int i) {
-  const uint32_t w = i == 0 ? x.x : i == 1 ? x.y : i == 2 ? x.z : x.w;
+// 16 values of a row to write: consecutive ones (half a 4-bit group), or for f16 pages two 16-byte
+// chunks half a row apart, so that the lanes' stores are consecutive.
+struct Piece {
+  uint4 v[2];
+};
+
+__device__ __forceinline__ uint32_t word_of(const Piece& x, int i) {
+  const uint4& v = x.v[i >> 2];
+  return (i & 3) == 0 ? v.x : (i & 3) == 1 ? v.y : (i & 3) == 2 ? v.z : v.w;
+}
+__device__ __forceinline__ __half2 half2_at(const Piece& x, int i) {
+  const uint32_t w = word_of(x, i);
   return *reinterpret_cast<const __half2*>(&w);
 }
 
-// Stores piece `ch` (8 values) of the row at `dst` with its scale(s) at `scale`: all lanes take
-// part in the shuffles, `ok` ones store.
+// Stores piece `ch` of the row at `dst` with its scale(s) at `scale`: all lanes take part in the
+// shuffles, `ok` ones store.
 template <int FMT, int D>
-__device__ __forceinline__ void store_piece(const uint4& x, char* dst, char* scale, int ch, bool ok) {
+__device__ __forceinline__ void store_piece(const Piece& x, char* dst, char* scale, int ch, bool ok) {
   if constexpr (FMT == QSA_PAGE_F16) {
-    if (ok) reinterpret_cast<uint4*>(dst)[ch] = x;
+    if (ok) {
+      reinterpret_cast<uint4*>(dst)[ch] = x.v[0];
+      reinterpret_cast<uint4*>(dst)[ch + D / 16] = x.v[1];
+    }
   } else if constexpr (FMT == QSA_PAGE_FP8) {
-    __half2 h = __hmax2(__hmax2(__habs2(half2_at(x, 0)), __habs2(half2_at(x, 1))),
-                        __hmax2(__habs2(half2_at(x, 2)), __habs2(half2_at(x, 3))));
+    __half2 h = __habs2(half2_at(x, 0));
 #pragma unroll
-    for (int off = D / 16; off >= 1; off >>= 1) h = __hmax2(h, __shfl_xor_sync(0xffffffffu, h, off));
+    for (int i = 1; i < 8; ++i) h = __hmax2(h, __habs2(half2_at(x, i)));
+#pragma unroll
+    for (int off = D / 32; off >= 1; off >>= 1) h = __hmax2(h, __shfl_xor_sync(0xffffffffu, h, off));
     const float top = fmaxf(__low2float(h), __high2float(h));
     const float factor = top > 0.0f ? __fmul_rn(448.0f, 1.0f / top) : 0.0f;
-    uint32_t codes[4];
+    uint32_t codes[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float2 v = __half22float2(half2_at(x, i));
       codes[i] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(v.x, factor), __fmul_rn(v.y, factor)), __NV_SATFINITE,
                                           __NV_E4M3);
     }
     if (ok) {
-      reinterpret_cast<uint2*>(dst)[ch] = make_uint2(__byte_perm(codes[0], codes[1], 0x5410), __byte_perm(codes[2], codes[3], 0x5410));
+      reinterpret_cast<uint4*>(dst)[ch] =
+          make_uint4(__byte_perm(codes[0], codes[1], 0x5410), __byte_perm(codes[2], codes[3], 0x5410),
+                     __byte_perm(codes[4], codes[5], 0x5410), __byte_perm(codes[6], codes[7], 0x5410));
       if (ch == 0) *reinterpret_cast<float*>(scale) = top > 0.0f ? __fmul_rn(top, 1.0f / 448.0f) : 1.0f;
     }
   } else {
-    // the largest |x| of the group (4 lanes): a NaN or an infinity comes through
-    __half2 h = __hmax2_nan(__hmax2_nan(__habs2(half2_at(x, 0)), __habs2(half2_at(x, 1))),
-                            __hmax2_nan(__habs2(half2_at(x, 2)), __habs2(half2_at(x, 3))));
+    // the largest |x| of the group (2 lanes): a NaN or an infinity comes through
+    __half2 h = __habs2(half2_at(x, 0));
+#pragma unroll
+    for (int i = 1; i < 8; ++i) h = __hmax2_nan(h, __habs2(half2_at(x, i)));
     h = __hmax2_nan(h, __shfl_xor_sync(0xffffffffu, h, 1));
-    h = __hmax2_nan(h, __shfl_xor_sync(0xffffffffu, h, 2));
     const __half top = __hmax_nan(__low2half(h), __high2half(h));
     const __half s = __half_as_ushort(top) >= 0x7c00u ? __ushort_as_half(0x7fff)
                                                       : __float2half_rn(__fmul_rn(__half2float(top), 1.0f / 7.0f));
@@ -122,28 +140,34 @@ __device__ __forceinline__ void store_piece(const uint4& x, char* dst, char* sca
     // rint(y) + 8 in the low bits of y + (1.5 * 2^23 + 8): the sum rounds to a whole number, to
     // even at ties. |y| is below 7.5 unless the scale lost bits (a subnormal f16): then clamped.
     const bool coarse = sf < 6.1e-5f;
-    uint32_t y[8];
+    uint32_t y[16];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float2 v = __half22float2(half2_at(x, i >> 1));
-      float f = __fmul_rn((i & 1) ? v.y : v.x, inv);
-      if (coarse) f = fminf(fmaxf(f, -7.0f), 7.0f);
-      y[i] = __float_as_uint(__fadd_rn(f, 12582920.0f));
+      const float2 v = __half22float2(half2_at(x, i));
+      float f0 = __fmul_rn(v.x, inv), f1 = __fmul_rn(v.y, inv);
+      if (coarse) {
+        f0 = fminf(fmaxf(f0, -7.0f), 7.0f);
+        f1 = fminf(fmaxf(f1, -7.0f), 7.0f);
+      }
+      y[2 * i] = __float_as_uint(__fadd_rn(f0, 12582920.0f));
+      y[2 * i + 1] = __float_as_uint(__fadd_rn(f1, 12582920.0f));
     }
-    uint32_t codes[2];
+    uint32_t codes[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 4; ++i) {
       codes[i] = __byte_perm(__byte_perm(y[4 * i], y[4 * i + 1], 0x0040), __byte_perm(y[4 * i + 2], y[4 * i + 3], 0x0040), 0x5410);
       codes[i] &= 0x0f0f0f0fu;
-      // dims + 16 of the group, two lanes on, into the high halves
-      codes[i] |= __shfl_down_sync(0xffffffffu, codes[i], 2) << 4;
+      // dims + 16 of the group, the next lane's, into the high halves
+      codes[i] |= __shfl_down_sync(0xffffffffu, codes[i], 1) << 4;
     }
-    if (ok && (ch & 3) < 2) reinterpret_cast<uint2*>(dst + (ch >> 2) * 16)[ch & 1] = make_uint2(codes[0], codes[1]);
-    if (ok && (ch & 3) == 0) reinterpret_cast<__half*>(scale)[ch >> 2] = s;
+    if (ok && (ch & 1) == 0) {
+      reinterpret_cast<uint4*>(dst)[ch >> 1] = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+      reinterpret_cast<__half*>(scale)[ch >> 1] = s;
+    }
   }
 }
 
-// What piece `ch` of a stored row is read from, and its values.
+// What piece `ch` (8 values) of a stored row is read from, and its values.
 template <int FMT>
 struct StoredPiece {
   uint4 codes;
@@ -188,7 +212,7 @@ __device__ __forceinline__ uint4 values_of(const StoredPiece<FMT>& p, int ch) {
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// Piece e of a CTA's tokens is piece e % (heads * D/8) of token e / (heads * D/8): a thread's
+// Piece e of a CTA's tokens is piece e % per_token of token e / per_token: a thread's
 // pieces are kRowThreads apart, so one division serves them all.
 struct PieceCursor {
   int per_token, tok, in, step_tok, step_in;
@@ -211,7 +235,7 @@ struct PieceCursor {
 template <int FMT, int D>
 __global__ void __launch_bounds__(kRowThreads) paged_write_kernel(PagedView c, PagedRows r, const __half* __restrict__ k,
                                                                   const __half* __restrict__ v, int tokens) {
-  constexpr int CH = D / 8;
+  constexpr int CH = D / 16;
   __shared__ TokenPlace s_at[kRowTokens];
   pdl_launch_dependents();
   pdl_wait();
@@ -222,15 +246,19 @@ __global__ void __launch_bounds__(kRowThreads) paged_write_kernel(PagedView c, P
   bool found = false;
   do {  // (the same trips in every thread: all take part in the shuffles)
     // the rows come while the CTA finds their places
-    uint4 x[kRowBatch], y[kRowBatch];
+    Piece x[kRowBatch], y[kRowBatch];
     PieceCursor q = p;
 #pragma unroll
     for (int i = 0; i < kRowBatch; ++i) {
-      x[i] = y[i] = make_uint4(0, 0, 0, 0);
+      x[i] = y[i] = Piece{};
       if (q.tok < n) {
-        const int64_t off = (t0 + q.tok) * r.row_stride + q.in * 8;
-        x[i] = *reinterpret_cast<const uint4*>(k + off);
-        y[i] = *reinterpret_cast<const uint4*>(v + off);
+        const int head = q.in / CH, ch = q.in % CH;
+        const int64_t off = (t0 + q.tok) * r.row_stride + head * D + ch * (FMT == QSA_PAGE_F16 ? 8 : 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          x[i].v[h] = reinterpret_cast<const uint4*>(k + off)[h * (FMT == QSA_PAGE_F16 ? CH : 1)];
+          y[i].v[h] = reinterpret_cast<const uint4*>(v + off)[h * (FMT == QSA_PAGE_F16 ? CH : 1)];
+        }
       }
       q.next();
     }
@@ -263,10 +291,10 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(PagedView c, Pa
   // bytes from a head's rows (scales) of a page to the next one's
   const int head_rows = page_row_bytes_c<FMT>(D) << c.page_shift, head_scales = page_scale_bytes_c<FMT>(D) << c.page_shift;
   while (p.tok < n) {
-    StoredPiece<FMT> x[kRowBatch], y[kRowBatch];
+    StoredPiece<FMT> x[kReadBatch], y[kReadBatch];
     PieceCursor q = p;
 #pragma unroll
-    for (int i = 0; i < kRowBatch; ++i) {
+    for (int i = 0; i < kReadBatch; ++i) {
       x[i] = y[i] = StoredPiece<FMT>{};
       if (q.tok < n) {
         const TokenPlace at = s_at[q.tok];
@@ -280,7 +308,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(PagedView c, Pa
       q.next();
     }
 #pragma unroll
-    for (int i = 0; i < kRowBatch; ++i) {
+    for (int i = 0; i < kReadBatch; ++i) {
       const int64_t at = p.tok < n ? s_at[p.tok].rows : -2;
       if (at != -2) {  // (padding rows stay as they are)
         const int64_t off = (t0 + p.tok) * r.row_stride + p.in * 8;
@@ -297,7 +325,7 @@ __global__ void __launch_bounds__(kRowThreads) paged_read_kernel(PagedView c, Pa
 // pieces a thread: finding places costs two rounds of loads, which the other CTAs hide.
 int row_tokens(const PagedView& c, const PagedRows& r, int n_sms) {
   const int spread = (r.n_rows + 4 * n_sms - 1) / (4 * n_sms);
-  const int full = 2 * kRowBatch * kRowThreads / (c.n_kv_heads * (c.head_dim / 8));
+  const int full = 2 * kRowThreads / (c.n_kv_heads * (c.head_dim / 16));
   const int most = full < kRowTokens ? full : kRowTokens;
   const int t = spread < most ? spread : most;
   return t < 1 ? 1 : t;

@@ -6,13 +6,14 @@
 // One pass over K and V with a running maximum and sum, split over the whole batch:
 //  - The (sequence, KV head) segments of a batch, cut into tiles of cells (a segment's start
 //    counts as two more), form one list; team i of N takes the i-th N-th of it (found from
-//    seq_lens on the device), so ragged batches and single long sequences load every SM alike. A segment cut by a border is written
-//    as partials (m, l, o), at most two a team, which paged_merge_kernel joins:
-//    sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Whole segments are written directly.
+//    seq_lens on the device), so ragged batches and single long sequences load every SM alike.
+//    A segment cut by a border is written as partials (m, l, o), at most two a team, which
+//    paged_merge_kernel joins: sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Whole segments
+//    are written directly.
 //  - One CTA an SM: two or three teams of four warps, each with its own share of the list, and
 //    a warpgroup whose warps load for one team each and leave their registers to the teams.
 //    Tiles of 64 cells come into the team's ring in shared memory (TMA tiles of a head's rows
-//    of a page, scales by bulk copies) across the segments' borders, so that the loads do not
+//    of a page, scales by 16-byte copies of the loading lanes) across the segments' borders, so that the loads do not
 //    pause while a segment's results are joined. Each warp of the team takes 16 cells of a
 //    tile, with no barrier between warps inside a segment. The products run on the tensor
 //    cores, transposed: S^T = K q^T and O^T = V^T P^T, cells resp. dims as the 16 MMA rows
