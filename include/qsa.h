@@ -340,7 +340,8 @@ qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, 
  *                for drafts without probabilities (looked up, or the draft model's argmax):
  *                q_i is then 1 at d_i and 0 elsewhere. A stride of 0 means vocab;
  *   draft_tokens [n_seqs][max_drafts] i32. An id outside [0, vocab) is rejected, its q_i
- *                taken as 0 if there are no draft probabilities, and reported;
+ *                taken as 0 if there are no draft probabilities, and reported where it is
+ *                reached (every draft before it accepted);
  *   n_drafts     [n_seqs] i32 or NULL; a value outside [0, max_drafts] is clamped and reported;
  *   uniforms     [n_seqs][max_drafts + 1] f32 in [0, 1): u_0.., and u_last in the last place
  *                whatever n is (a negative number or NaN counts as 0);
@@ -374,7 +375,7 @@ qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, c
  *   QSA_PAGE_FP8:  e4m3 codes and one f32 scale = amax * f32(1/448); code = e4m3(x * (448 *
  *     (1 / amax))) in f32, rounded to nearest even and saturated; an all-zero row has scale 1
  *     (QSA_KV_FP8 up to the last bit of the factors: one division a row instead of two).
- *     Value code * scale.
+ *     Value code * scale. A row that holds an infinity reads back as NaN.
  *   QSA_PAGE_INT4: groups of 32 dims with one f16 scale s = f16(amax * f32(1/7)); code =
  *     rint(x * (1 / s)) in f32, clamped to [-7, 7], 0 if s = 0; stored as code + 8 (4 bits).
  *     Byte j < 16 of a group holds dim j in its low and dim j + 16 in its high half. Value

@@ -560,6 +560,48 @@ def test_captured_steps_replay_with_other_lengths(fmt):
         assert int(p.status) == 0
 
 
+_FIRST_CALLS = """
+import sys
+sys.path.insert(0, %r)
+import torch
+import sparse_attention_decode_02_b200 as Q
+i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+c = Q.alloc_paged_kv(8, 32, 2, 64, Q.QSA_PAGE_INT4)
+k, v = (torch.randn(100, 2, 64, device="cuda").half() for _ in range(2))
+x, y = torch.zeros_like(k), torch.zeros_like(v)
+q, out = torch.randn(1, 3, 10, 64, device="cuda").half(), torch.zeros(1, 3, 10, 64, device="cuda")
+table, first, start, lens, status = i32([[3, 1, 6, 2]]), i32([0]), i32([0, 100]), i32([100]), i32([0])
+ws = torch.empty(c.workspace_bytes(10, 3), dtype=torch.uint8, device="cuda")
+p, u = torch.full((1, 2, 50), 0.02, device="cuda"), torch.full((1, 2), 0.51, device="cuda")
+m, t, d = i32([9]), i32([9]), i32([[0]])
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    c.write(k, v, table, first, start, status=status)
+    c.attend(q, table, lens, out, ws, status=status)
+    c.read(x, y, table, first, start, status=status)
+    Q.verify_drafts(p, None, d, u, m, t, status=status)
+g.replay()
+torch.cuda.synchronize()
+z = torch.einsum("uhd,nhd->uhn", q[0].float(), x.float().repeat_interleave(5, 1)) / 8
+z = z.masked_fill(torch.arange(100, device="cuda") > 97 + torch.arange(3, device="cuda")[:, None, None], float("-inf"))
+want = torch.einsum("uhn,nhd->uhd", z.softmax(-1), y.float().repeat_interleave(5, 1))
+assert torch.allclose(out[0], want, atol=1e-5), (out[0] - want).abs().max()
+assert int(status) == 0 and int(m) == 0 and int(t) == 25, (int(status), int(m), int(t))
+print("first calls captured")
+"""
+
+
+def test_first_calls_of_a_process_may_be_captured():
+    """Nothing that a first call does (attributes, descriptors, loading the kernels) breaks a capture."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST_CALLS % root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "first calls captured" in r.stdout, r.stdout + r.stderr
+
+
 def test_two_streams_with_a_workspace_each():
     pools = [Pool([6000, 5], "f16", 4, 128, 64, seed=i) for i in range(2)]
     streams = [torch.cuda.Stream() for _ in pools]
