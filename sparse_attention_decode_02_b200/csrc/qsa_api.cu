@@ -584,11 +584,11 @@ qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, c
       !usable(next_token, 4) || !aligned(n_drafts, 4) || !aligned(status, 4) ||
       (max_drafts > 0 && !usable(draft_tokens, 4)))
     return QSA_ERR_INVALID_ARG;
-  int n_sms = 0;
-  if (!current_sms(&n_sms)) return QSA_ERR_CUDA;
+  int n_sms = 0, device = 0;
+  if (!current_sms(&n_sms, &device)) return QSA_ERR_CUDA;
   const VerifyArgs a{target_probs, target_stride, draft_probs, draft_stride, draft_tokens, n_drafts, uniforms,
                      n_seqs,       max_drafts,    vocab,       n_accepted,   next_token,   status};
-  return status_of(launch_verify(a, n_sms, (cudaStream_t)stream));
+  return status_of(launch_verify(a, n_sms, device, (cudaStream_t)stream));
 }
 
 size_t qsa_paged_bytes(const qsa_paged_kv* cache, int32_t which) {

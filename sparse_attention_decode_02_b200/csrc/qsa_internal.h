@@ -238,7 +238,7 @@ struct VerifyArgs {
   int32_t* next_token;
   int32_t* status;
 };
-cudaError_t launch_verify(const VerifyArgs& a, int n_sms, cudaStream_t s);
+cudaError_t launch_verify(const VerifyArgs& a, int n_sms, int device, cudaStream_t s);
 
 // set_state modes
 enum { kSetReset = 0, kSetRestore = 1, kSetInvalidate = 2, kSetClearStatus = 3, kSetRollback = 4 };

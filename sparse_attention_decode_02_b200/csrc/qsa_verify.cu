@@ -10,9 +10,11 @@
 // chain token -> its probabilities -> row -> sums -> token. A cluster of CTAs shares a row, as
 // many as fill the GPU; their sums meet in distributed shared memory, so that one launch does.
 // Measured on B200 (us; share of a copy's 6,568 GB/s): 64 sequences x 151,936 tokens 19 (49%),
-// 256 x 100,003 40 (73%), one x 32,000 4.8. The small ones are that chain: about 7 us of it.
+// 256 x 100,003 40 (73%), one x 32,000 4.4, one x 151,936 6.8. The small ones are that chain.
 // Sums are f64: among 150,000 weights an f32 sum is off by more than the small weights, and
 // the token would depend on the order.
+#include <atomic>
+
 #include <cooperative_groups.h>
 
 #include "qsa_device.cuh"
@@ -26,7 +28,7 @@ namespace {
 constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfPerSm = 4;                // CTAs an SM holds (60 registers a thread)
-constexpr int kVfMaxCluster = 8;
+constexpr int kVfMaxCluster = 16;
 constexpr int kVfBatch = 8;                // tokens a lane has in flight from each row
 constexpr int kVfBlock = 32 * kVfBatch;    // tokens of a warp's batch
 
@@ -267,12 +269,24 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyArgs a) {
 
 }  // namespace
 
-cudaError_t launch_verify(const VerifyArgs& a, int n_sms, cudaStream_t s) {
+cudaError_t launch_verify(const VerifyArgs& a, int n_sms, int device, cudaStream_t s) {
   // CTAs a sequence: as many (a power of two) as the GPU holds at once for the whole batch, with
   // a token for every thread. At 64 x 151,936 tokens 8 CTAs take 19 us (512-thread CTAs, of
-  // which an SM holds two, 33); at 256 x 100,003 2 take 40 us and 4, in two waves, 47.
+  // which an SM holds two, 33); at 256 x 100,003 2 take 40 us and 4, in two waves, 47. Clusters
+  // of 16, which fit fewer places, only up to half of that: 12 sequences 9.5 us against 10.4
+  // with 8, one 6.8 against 9.7, but 36 sequences 19 against 17.6.
   int size = kVfMaxCluster;
+  if (2LL * a.n_seqs * size > kVfPerSm * (long long)n_sms) size /= 2;
   while (size > 1 && ((long long)a.n_seqs * size > kVfPerSm * (long long)n_sms || a.vocab < size * kVfThreads)) size /= 2;
+  if (size > 8) {  // more than the portable 8: allowed once a device
+    static std::atomic<unsigned long long> ready{0};
+    const unsigned long long bit = 1ull << (device & 63);
+    if (device >= 64 || !(ready.load(std::memory_order_acquire) & bit)) {
+      const cudaError_t e = cudaFuncSetAttribute(verify_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+      if (e != cudaSuccess) return e;
+      if (device < 64) ready.fetch_or(bit, std::memory_order_release);
+    }
+  }
   return launch_pdl(verify_kernel, dim3(a.n_seqs * size), dim3(kVfThreads), 0, s, size, a);
 }
 
