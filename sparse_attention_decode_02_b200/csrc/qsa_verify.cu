@@ -69,6 +69,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyArgs a) {
   const cg::cluster_group cluster = cg::this_cluster();
   const int size = int(cluster.num_blocks()), rank = int(cluster.block_rank());
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, seq = blockIdx.x / size;
+  cluster_arrive_relaxed();  // waited for before the first store into another CTA's shared memory
   pdl_launch_dependents();
   pdl_wait();
 
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyArgs a) {
   const double mine = warp_sum_f64(chunk_sum);
   if (lane == 0) s_sum[warp] = mine;
   __syncthreads();
+  cluster_wait();  // every CTA of the cluster has started: its shared memory may be written
   if (warp == 0 && lane < size) {  // this CTA's sum to every CTA of the cluster
     double all = 0.0;
 #pragma unroll

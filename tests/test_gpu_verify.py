@@ -97,6 +97,21 @@ def test_exact_thresholds(V):
     assert _verify(target, None, np.zeros((len(js), 0), np.int32), below) == [(0, max(j - 1, 0)) for j in js]
 
 
+def test_ctas_with_few_or_no_tokens_of_a_row():
+    """Vocabularies that leave the last CTAs of a cluster little or nothing to read: they reach
+    the exchange of the sums long before the others, launch after launch."""
+    rng = np.random.default_rng(12)
+    for S, V in ((1, 4097), (1, 4225), (5, 4096), (20, 2049), (40, 2111), (70, 1030)):
+        target, draft, tokens, u = _random(rng, S, 2, V)
+        want = [P.verify(target[i], draft[i], tokens[i], u[i]) for i in range(S)]
+        dev = [H.to_dev(x) for x in (target, draft, tokens, u)]
+        outs = [[torch.full((S,), -7, dtype=torch.int32, device="cuda") for _ in range(2)] for _ in range(40)]
+        for o in outs:
+            Q.verify_drafts(*dev, *o)
+        for o in outs:
+            assert list(zip(o[0].tolist(), o[1].tolist())) == want
+
+
 def test_all_weight_on_one_token():
     V = 70001
     for at in (0, 1, 35000, V - 1):
