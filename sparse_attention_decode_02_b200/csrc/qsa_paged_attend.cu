@@ -486,6 +486,12 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         parity ^= 1;
       }
     }
+    // The copies on their way land before the CTA's shared memory may become another's, even if
+    // the computing warps have given up waiting: slots before `slot` were last filled in this
+    // round of the ring, the others in the one before (or never, which counts as landed).
+#pragma unroll 1
+    for (int i = 0; i < STAGES; ++i)
+      if (!sm100::mbar_wait(&sm.full[i], i < slot ? parity ^ 1 : parity)) break;
     return;
   }
 
