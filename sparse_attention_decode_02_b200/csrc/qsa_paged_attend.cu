@@ -8,7 +8,7 @@
 //    counts as two more), form one list; team i of N takes the i-th N-th of it (found from
 //    seq_lens on the device), so ragged batches and single long sequences load every SM alike.
 //    A segment cut by a border is written as partials (m, l, o), at most two a team, which
-//    paged_merge_kernel joins: sum_s 2^(m_s - M) o_s / sum_s 2^(m_s - M) l_s. Whole segments
+//    paged_merge_kernel joins: sum_s w_s o_s / sum_s w_s l_s, w_s = exp(scale (m_s - M)). Whole segments
 //    are written directly.
 //  - One CTA an SM: two or three teams of four warps, each with its own share of the list, and
 //    a warpgroup whose warps load for one team each and leave their registers to the teams.
@@ -57,6 +57,8 @@ constexpr int kPaStart = 2;                  // a segment's start (queries, join
 // at most 2^8; times 2^7 they fill f16's range (below 2^16).
 constexpr float kPaSlack = 8.0f;
 constexpr float kPaTop = 128.0f;
+constexpr float kPaNone = -3e38f;  // the running maximum before the first cell: finite, so that -inf - it is -inf
+constexpr float kLog2e = 1.44269504088896341f, kLn2 = 0.693147180559945309f;
 
 template <int FMT, int D, int NC>
 struct PaCfg {
@@ -87,6 +89,11 @@ struct PaCfg {
   static constexpr int BYTES = TEAMS * (RING + SRING + JOIN + Q + SMALL);
   static_assert(STAGES >= 2, "the ring needs two tiles");
   static_assert(KB % 1024 == 0, "swizzled tiles start on their pattern's border");
+};
+
+// sm_scale for base-2 exponents, and kPaSlack in units of q.K (as arguments they take no registers).
+struct PaExp {
+  float c1, slack;
 };
 
 // What merge CTA i joins: if the batch has no more segments than teams, segment i (written by
@@ -131,6 +138,10 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+// log sum exp from the largest q.K and the sum of the weights relative to it.
+__device__ __forceinline__ float lse_of(float top, float sum, float sm_scale) {
+  return sum == 0.0f ? -INFINITY : fmaf(top, sm_scale, log2f(sum) * kLn2);
 }
 __device__ __forceinline__ uint32_t as_u32(__half2 h) { return *reinterpret_cast<uint32_t*>(&h); }
 __device__ __forceinline__ __half2 as_h2(uint32_t u) { return *reinterpret_cast<__half2*>(&u); }
@@ -273,7 +284,7 @@ static_assert(sizeof(PaSmall) <= 4096, "PaCfg::SMALL");
 template <int FMT, int D, int NC>
 __global__ void __launch_bounds__(PaCfg<FMT, D, NC>::THREADS, 1)
 paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap, PagedView c,
-                    PagedAttendArgs a, float* __restrict__ part, PaSplit* __restrict__ splits) {
+                    PagedAttendArgs a, PaExp ex, float* __restrict__ part, PaSplit* __restrict__ splits) {
   using C = PaCfg<FMT, D, NC>;
   constexpr int KS = C::KS, STAGES = C::STAGES, ROW = C::ROW, SROW = C::SROW, TEAMS = C::TEAMS;
   constexpr int ALL = C::THREADS;
@@ -498,7 +509,10 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   // =============================== computing warps ===============================
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(C::REGS_TEAM));
   const int g = lane >> 2, t = lane & 3;
-  const float c1 = a.sm_scale * 1.44269504088896341f;  // logits in units of log 2
+  // p = 2^((s - top) c1). The difference comes first: it is exact near the maximum, while in
+  // s c1 - top c1 the rounding of one product is 2^-24 of a logit, which for large ones is
+  // more than an exponent.
+  const float c1 = ex.c1, slack = ex.slack;
   const bool by_segment = (long long)a.n_seqs * Hkv <= n_teams;
   if (tid == 0) {
     // the first team that continues a segment names the parts to merge
@@ -570,16 +584,16 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       for (int e = tid; e < KS * NC * 32; e += kPaThreads) s_q[e] = q_frag(e / (32 * NC), (e / 32 % NC) * 8 + g, t);
       sm100::named_bar_sync(1 + team, kPaThreads);
     }
-    // Per column: exponents are taken from `base` (minus the running maximum times c1, 0 while
-    // there is none), which is renewed when a logit passes `limit`.
-    float base[NC][2], limit[NC][2], l[NC][2], acc[KS][NC][4];
+    // Per column: exponents are taken from `top`, the running maximum of q.K, which is renewed
+    // when one passes it by `slack`.
+    float top[NC][2], l[NC][2], acc[KS][NC][4];
     float vtop = 0x1p-60f;  // power of two, at least the largest V scale so far (e4m3)
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        base[n][i] = l[n][i] = 0.0f;
-        limit[n][i] = -INFINITY;
+        top[n][i] = kPaNone;
+        l[n][i] = 0.0f;
       }
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -757,7 +771,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
         for (int n = 0; n < NC; ++n)
 #pragma unroll
-          for (int i = 0; i < 2; ++i) over |= fmaxf(s[n][i], s[n][2 + i]) > limit[n][i];
+          for (int i = 0; i < 2; ++i) over |= fmaxf(s[n][i], s[n][2 + i]) - top[n][i] > slack;
         if (__any_sync(0xffffffffu, over)) {
 #pragma unroll
           for (int n = 0; n < NC; ++n)
@@ -766,18 +780,13 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               float x = fmaxf(s[n][i], s[n][2 + i]);
 #pragma unroll
               for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, off));
-              const bool none = limit[n][i] == -INFINITY;
-              const float to = none ? -x * c1 : fminf(base[n][i], -x * c1);
-              if (x != -INFINITY) {  // (else this column has seen nothing here)
-                const float corr = none ? 0.0f : ex2(to - base[n][i]);
-                base[n][i] = to;
-                limit[n][i] = (kPaSlack - to) / c1;
-                l[n][i] *= corr;
+              const float to = fmaxf(top[n][i], x), corr = ex2((top[n][i] - to) * c1);
+              top[n][i] = to;
+              l[n][i] *= corr;
 #pragma unroll
-                for (int k = 0; k < KS; ++k) {
-                  acc[k][n][i] *= corr;
-                  acc[k][n][2 + i] *= corr;
-                }
+              for (int k = 0; k < KS; ++k) {
+                acc[k][n][i] *= corr;
+                acc[k][n][2 + i] *= corr;
               }
             }
         }
@@ -789,7 +798,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           for (int r = 0; r < 2; ++r) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              const float p = ex2(fmaf(s[n][2 * r + i], c1, base[n][i]));
+              const float p = ex2((s[n][2 * r + i] - top[n][i]) * c1);
               l[n][i] += p;
               s[n][2 * r + i] = p * vf[r];
             }
@@ -888,7 +897,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) l[n][i] += __shfl_xor_sync(0xffffffffu, l[n][i], off);
         if (g == 0) {
-          sm.m[warp][n * 8 + 2 * t + i] = -base[n][i];  // the maximum in log 2 units, where l > 0
+          sm.m[warp][n * 8 + 2 * t + i] = top[n][i];  // the maximum, where l > 0
           sm.l[warp][n * 8 + 2 * t + i] = l[n][i];
         }
       }
@@ -908,7 +917,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
       for (int w = 0; w < kPaWarps; ++w) {
         const float lw = sm.l[w][tid];
-        fw[w] = lw == 0.0f ? 0.0f : ex2(sm.m[w][tid] - M);
+        fw[w] = lw == 0.0f ? 0.0f : ex2((sm.m[w][tid] - M) * c1);
         L += fw[w] * lw;
       }
       const float end = complete ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
@@ -919,7 +928,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         out_part[tid * (D + 4) + D] = M;
         out_part[tid * (D + 4) + D + 1] = L;
       } else if (a.lse) {
-        a.lse[out_row + sm.out_off[tid]] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+        a.lse[out_row + sm.out_off[tid]] = lse_of(M, L, a.sm_scale);
       }
     }
     sm100::named_bar_sync(1 + team, kPaThreads);
@@ -976,7 +985,8 @@ constexpr int kPmBatch = 14;
 
 template <int D>
 __global__ void __launch_bounds__(32 * kPmWarps) paged_merge_kernel(PagedAttendArgs a, const float* __restrict__ part,
-                                                                    const PaSplit* __restrict__ splits, int n_kv_heads) {
+                                                                    const PaSplit* __restrict__ splits, int n_kv_heads,
+                                                                    float c1) {
   constexpr int V = D / 32;
   __shared__ float s_o[kPmWarps][D], s_ml[kPmWarps][2];
   pdl_launch_dependents();
@@ -998,7 +1008,7 @@ __global__ void __launch_bounds__(32 * kPmWarps) paged_merge_kernel(PagedAttendA
     // adds m, l, x (a part that saw nothing has l = 0)
     const auto add = [&](float m, float l, const float* x) {
       if (l == 0.0f) return;
-      const float to = fmaxf(M, m), keep = M == to ? 1.0f : ex2(M - to), w = m == to ? 1.0f : ex2(m - to);
+      const float to = fmaxf(M, m), keep = M == to ? 1.0f : ex2((M - to) * c1), w = m == to ? 1.0f : ex2((m - to) * c1);
       M = to;
       L = L * keep + w * l;
 #pragma unroll
@@ -1040,7 +1050,7 @@ __global__ void __launch_bounds__(32 * kPmWarps) paged_merge_kernel(PagedAttendA
       float* const to = a.out + row * D + lane * V;
       if constexpr (V == 4) *reinterpret_cast<float4*>(to) = *reinterpret_cast<const float4*>(o);
       else *reinterpret_cast<float2*>(to) = *reinterpret_cast<const float2*>(o);
-      if (a.lse && lane == 0) a.lse[row] = L == 0.0f ? -INFINITY : (M + log2f(L)) * 0.693147180559945309f;
+      if (a.lse && lane == 0) a.lse[row] = lse_of(M, L, a.sm_scale);
     }
   }
 }
@@ -1105,15 +1115,17 @@ cudaError_t launch_pa(const PagedView& c, const PagedAttendArgs& a, int n_sms, i
   if (e == cudaSuccess) e = encode_pages(c, FMT, c.v, rows, &vmap);
   if (e != cudaSuccess) return e;
   const int ctas = paged_ctas(n_sms, C::TEAMS), n = ctas * C::TEAMS, R = a.n_q_heads / c.n_kv_heads * a.n_queries;
+  const float c1 = a.sm_scale * kLog2e;
+  const PaExp x{c1, kPaSlack / c1};
   PaSplit* splits = static_cast<PaSplit*>(a.workspace);
   float* part = reinterpret_cast<float*>(static_cast<char*>(a.workspace) + align256(n * sizeof(PaSplit)));
-  e = launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::BYTES, s, 1, kmap, vmap, c, a, part, splits);
+  e = launch_pdl(kernel, dim3(ctas), dim3(C::THREADS), C::BYTES, s, 1, kmap, vmap, c, a, x, part, splits);
   if (e != cudaSuccess) return e;
   // one merge CTA for each segment that may be cut, or several where they are few
   const long long segments = (long long)a.n_seqs * c.n_kv_heads;
-  const int x = segments < n ? int(segments) : n, y = min(R, max(1, 2 * n_sms / x));
-  return launch_pdl(paged_merge_kernel<D>, dim3(x, y), dim3(32 * kPmWarps), 0, s, 1, a, (const float*)part,
-                    (const PaSplit*)splits, c.n_kv_heads);
+  const int nx = segments < n ? int(segments) : n, ny = min(R, max(1, 2 * n_sms / nx));
+  return launch_pdl(paged_merge_kernel<D>, dim3(nx, ny), dim3(32 * kPmWarps), 0, s, 1, a, (const float*)part,
+                    (const PaSplit*)splits, c.n_kv_heads, x.c1);
 }
 
 template <int FMT, int D>

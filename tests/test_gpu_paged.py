@@ -292,6 +292,78 @@ def test_attention_of_constant_rows():
     assert abs(float(lse[0, 0, 0]) - (z + np.log(1000))) <= 2 * abs(z) * UNIT
 
 
+def assert_exact_logits(out, lse, q, k, v, sm_scale=None, what=""):
+    """For queries and keys whose products and sums are exact in f32, whatever their size. The
+    exponent (s - max) sm_scale log2(e) is then off by four roundings of half a unit, and what
+    has an exponent below -150 has no weight in f32: 150 ln(2) 4 2^-24 and two units of the
+    exponential make the error of a weight."""
+    want, want_lse, bound, _ = P.attention(q, k, v, sm_scale)
+    n = len(k)
+    e = 150 * np.log(2) * 2 * UNIT + 2 * UNIT
+    tol = (2 * e + (n + 64) * UNIT) * bound + n * 2.0 ** -32 * np.abs(v).max()
+    assert np.isfinite(out).all() and np.isfinite(lse).all(), f"{what}: not finite"
+    assert (np.abs(out - want) <= tol).all(), f"{what}: {np.max(np.abs(out - want) / tol):.3g} of tolerance"
+    assert (np.abs(lse - want_lse) <= 2 * UNIT * np.abs(want_lse) + e + (n + 64) * UNIT).all(), f"{what}: lse"
+
+
+HUGE = [([5000], 1), ([37, 700, 1], 1), ([20, 5], 4), ([900], 3), ([33] * 460, 1)]
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("lens,T", HUGE)
+@pytest.mark.parametrize("sm_scale", [0.0, 1.0, 1e4, 1e20])
+def test_logits_of_any_size(fmt, lens, T, sm_scale):
+    """Logits as large as f16 rows and an accepted scale make them, equal and not, in whole
+    segments and in segments cut into parts: the largest ones share the weight."""
+    p = Pool(lens, fmt, 1, 128, 16, seed=len(lens))
+    n = sum(lens)
+    k, v = np.zeros((n, 1, 128), np.float16), p.random_rows(lens)[1]
+    k[..., 1] = 57344                           # makes every scale a power of two: stored exactly
+    k[..., 0] = p.rng.choice([57344, 49152], (n, 1))
+    p.append(lens, (k, v))
+    assert all((p.values(i)[0] == p.rows[0][i]).all() for i in range(len(lens)))
+    q = np.zeros((len(lens), T, 4, 128), np.float16)
+    q[..., 0] = p.rng.choice([60000, -60000, 30000, 2.0 ** -14], (len(lens), T, 4))
+    out, lse = (x.cpu().numpy().astype(np.float64) for x in p.attend(q, sm_scale=sm_scale))
+    assert int(p.status) == 0
+    for i in range(len(lens)):
+        kk, vv = p.values(i)
+        assert_exact_logits(out[i], lse[i], q[i], kk, vv, sm_scale, f"sequence {i}")
+
+
+@pytest.mark.parametrize("value", [100, 2000, 8000, 30000, 65504])
+@pytest.mark.parametrize("n,T", [(10, 1), (5000, 1), (700, 4)])
+def test_equal_logits_of_any_size(value, n, T):
+    """Rows and queries of one value: every cell has the same weight, however large the logit."""
+    p = Pool([n], "f16", 1, 128, 64, seed=n)
+    k, v = np.full((n, 1, 128), value, np.float16), p.random_rows([n])[1]
+    p.append([n], (k, v))
+    q = np.full((1, T, 8, 128), value, np.float16)
+    out, lse = (x.cpu().numpy().astype(np.float64)[0] for x in p.attend(q))
+    for u in range(T):
+        seen = n - T + u + 1
+        want, bound = v[:seen, 0].astype(np.float64).mean(0), np.abs(v[:seen, 0].astype(np.float64)).mean(0)
+        assert (np.abs(out[u] - want) <= (seen + 64) * UNIT * bound + 2.0 ** -32 * np.abs(v).max()).all()
+        # (the sum of 128 products is off by up to 128 units)
+        z = float(np.float16(value)) ** 2 * 128 / np.sqrt(128)
+        assert (np.abs(lse[u] - (z + np.log(seen))) <= 130 * UNIT * z + (seen + 64) * UNIT).all()
+
+
+@pytest.mark.parametrize("step", [2.0 ** 25, 2.0 ** 27, 2.0 ** 29])
+def test_large_logits_that_differ_by_their_last_bits(step):
+    """q.K = step + the smallest f32 differences from it: the weights are those of the differences."""
+    n = 300
+    p = Pool([n], "f16", 1, 128, 16, seed=7)
+    k, v = np.zeros((n, 1, 128), np.float16), p.random_rows([n])[1]
+    k[..., 0], k[..., 1] = 2.0 ** 14, p.rng.integers(0, 6, (n, 1)) * step * 2.0 ** -23
+    p.append([n], (k, v))
+    q = np.zeros((1, 1, 8, 128), np.float16)
+    q[..., 0], q[..., 1] = step / 2.0 ** 14, 1.0
+    for sm_scale in (1.0, 0.125, 0.01):
+        out, lse = (x.cpu().numpy().astype(np.float64) for x in p.attend(q, sm_scale=sm_scale))
+        assert_exact_logits(out[0], lse[0], q[0], *p.values(0), sm_scale, f"scale {sm_scale}")
+
+
 def test_a_logit_that_overflows_to_minus_infinity_has_no_weight():
     """q k beyond f32 is not reachable from f16 rows, but infinite keys are: -inf logits drop
     out, and a sequence with nothing else is empty."""
