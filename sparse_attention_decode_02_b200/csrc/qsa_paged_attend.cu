@@ -24,7 +24,8 @@
 //  - Precision: codes are exact in f16 (e4m3 scales multiply logits and weights in f32; a 4-bit
 //    value is an f16 product by definition). A weight enters the second product as two f16
 //    terms of 2^7 p (22 bits, down to 2^-32 of the largest), which costs a second MMA and
-//    keeps the result at f32 precision. The products of each 16 cells are added to the
+//    keeps the result at f32 precision; an e4m3 weight, p times the row's scale, relative to
+//    the largest scale of its 16 rows. The products of each 16 cells are added to the
 //    running output in f32: the MMA's own sums truncate, and over a long chain that adds up.
 //  - The newest T - 1 cells are not seen by every query, and an infinity or a NaN in them must
 //    not reach the others (0 * NaN is NaN): such a V row stays out of the MMA and is added to
@@ -67,11 +68,12 @@ struct PaCfg {
   static constexpr int KB = kPaTile * ROW;                 // bytes of a tile's K (V) rows
   static constexpr int SB = kPaTile * SROW;                // and of their scales
   static constexpr int KS = D / 16;                        // MMA k-steps of q.K = m-tiles of P.V
-  // Teams of a CTA (one CTA an SM): three where a thread's sums take up to 64 registers (f16
-  // rows: 32), two where they take more or 256-byte rows need the shared memory. One more
-  // warpgroup loads. (Two column groups of 128 dims: three teams take 116 us against 133 at
-  // 4 bits, 69 against 71 at e4m3; four groups of 64-dim f16 rows 43 against 41.)
-  static constexpr int TEAMS = KS * NC <= (FMT == QSA_PAGE_F16 ? 8 : 16) && ROW <= 128 ? 3 : 2;
+  // Teams of a CTA (one CTA an SM): three where a thread's sums take up to 32 registers (4-bit
+  // rows: 64), two where they take more or 256-byte rows need the shared memory. One more
+  // warpgroup loads. (100 sequences of up to 8,192, us: two column groups of 128 dims, three teams
+  // 154 against 169 at 4 bits, but 280 against 143 at e4m3, whose rows added one by one take
+  // registers too; three groups of 64-dim e4m3 rows 127 against 123.)
+  static constexpr int TEAMS = KS * NC <= (FMT == QSA_PAGE_INT4 ? 16 : 8) && ROW <= 128 ? 3 : 2;
   static constexpr int THREADS = kPaThreads * (TEAMS + 1);
   // registers a thread: at launch, and as the warpgroups split them
   static constexpr int REGS = TEAMS == 3 ? 128 : 168;
@@ -149,6 +151,9 @@ __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
   asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
   return v;
+}
+__device__ __forceinline__ void sts32(uint32_t a, uint32_t v) {
+  asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 __device__ __forceinline__ uint2 lds64(uint32_t a) {
   uint2 v;
@@ -276,8 +281,6 @@ struct PaSmall {
   int seq;
   unsigned lost[8];   // of each ring slot: bit w is set if warp w's cells have no page in the pool
   float m[kPaWarps][32], l[kPaWarps][32];  // statistics, then each warp's factor and 1 / l
-  float vtop[kPaWarps];
-  float newest[kPaWarps][QSA_MAX_QUERIES - 1][32];  // weights of the cells not every query sees
 };
 static_assert(sizeof(PaSmall) <= 4096, "PaCfg::SMALL");
 
@@ -548,6 +551,9 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   }
 
   const int w16 = warp * 16;  // this warp's rows of a tile
+  // weights [cell][column] of rows added one by one (the warp's part of s_join, unused between joins)
+  float* const stash = s_join + warp * 8 * (D + 4);
+  static_assert(16 * 32 <= 8 * (D + 4), "the warp's part holds a step's weights");
   const int pg = w16 + cell_of<FMT, D>(g);
   const int pv0 = w16 + cell_of<FMT, D>(2 * t), pv1 = w16 + cell_of<FMT, D>(2 * t + 1);
   int slot = 0;
@@ -587,7 +593,6 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     // Per column: exponents are taken from `top`, the running maximum of q.K, which is renewed
     // when one passes it by `slack`.
     float top[NC][2], l[NC][2], acc[KS][NC][4];
-    float vtop = 0x1p-60f;  // power of two, at least the largest V scale so far (e4m3)
 #pragma unroll
     for (int n = 0; n < NC; ++n) {
 #pragma unroll
@@ -724,34 +729,18 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         }
 
         // logits: times the row's scale (e4m3), masked
-        float vf[2] = {kPaTop, kPaTop};
+        uint32_t vf[2] = {0u, 0u};  // the rows' V scales (e4m3), as bits
         if constexpr (FMT == QSA_PAGE_FP8) {
 #pragma unroll
           for (int r = 0; r < 2; ++r) {
             const float f = __uint_as_float(lds32(uks + (pg + 8 * r) * 4));
-            vf[r] = __uint_as_float(lds32(uvs + (pg + 8 * r) * 4));
-            if ((zero >> (pg - w16 + 8 * r)) & 1) vf[r] = 0.0f;
+            vf[r] = lds32(uvs + (pg + 8 * r) * 4);
+            if ((zero >> (pg - w16 + 8 * r)) & 1) vf[r] = 0u;
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
               for (int i = 0; i < 2; ++i) s[n][2 * r + i] *= f;
           }
-          // weights enter the MMA relative to the largest V scale so far
-          if (__any_sync(0xffffffffu, fmaxf(vf[0], vf[1]) > vtop)) {
-            const float vmax = warp_max(fmaxf(vf[0], vf[1]));
-            const float top = __uint_as_float((__float_as_uint(vmax) + 0x7fffffu) & 0x7f800000u);
-            const float keep = vtop * __uint_as_float(0x7f000000u - __float_as_uint(top));
-            vtop = top;
-#pragma unroll
-            for (int k = 0; k < KS; ++k)
-#pragma unroll
-              for (int n = 0; n < NC; ++n)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) acc[k][n][i] *= keep;
-          }
-          const float fv = kPaTop * __uint_as_float(0x7f000000u - __float_as_uint(vtop));  // / 2^e by its exponent
-#pragma unroll
-          for (int r = 0; r < 2; ++r) vf[r] = ((apart >> (pg - w16 + 8 * r)) & 1) ? kPaTop : vf[r] * fv;
         }
         if (!whole) {
 #pragma unroll
@@ -790,27 +779,63 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               }
             }
         }
-        // weights; as B fragments of P^T: two f16 terms each
-        uint32_t ph[NC][2], pl[NC][2];
+        // weights
 #pragma unroll
-        for (int n = 0; n < NC; ++n) {
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const float p = ex2((s[n][2 * r + i] - top[n][i]) * c1);
               l[n][i] += p;
-              s[n][2 * r + i] = p * vf[r];
+              s[n][2 * r + i] = p;
             }
-            const float x = s[n][2 * r], y = s[n][2 * r + 1];
+
+        // An e4m3 weight is p times the row's scale. So that its two terms keep their bits it enters
+        // relative to a power of two next above the largest scale of the 16 rows, by which the
+        // product is scaled back as it is added. Rows with scales of less than 2^-8 of that are
+        // added one by one in f32, after all-zero rows (their scale is 1) are left out.
+        float w[2] = {kPaTop, kPaTop}, unit = 1.0f;
+        if constexpr (FMT == QSA_PAGE_FP8) {
+          bool low[2];
+          const auto choose = [&] {  // true: the scales lie too far apart
+            const uint32_t most = __reduce_max_sync(0xffffffffu, max(vf[0] & 0x7fffffffu, vf[1] & 0x7fffffffu));
+            // the bits of the power of two, 2^-119 (then no row is too small) to 2^126
+            const uint32_t e = max((min(most, 0x7e800000u) + 0x7fffffu) & 0x7f800000u, 0x04000000u);
+            unit = __uint_as_float(e) * (1.0f / kPaTop);
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              low[r] = vf[r] != 0u && (vf[r] & 0x7fffffffu) < e - 0x04000000u;
+              w[r] = low[r] ? 0.0f : __uint_as_float(vf[r]) * __uint_as_float(0x7f000000u - e) * kPaTop;
+            }
+            return __any_sync(0xffffffffu, low[0] || low[1]);
+          };
+          if (choose()) {
+            uint32_t codes = 0;  // of half a row a lane
+#pragma unroll 1
+            for (int b = 0; b < ROW / 2; b += 4)
+              codes |= lds32(uv + swizzled((w16 + (lane >> 1)) * ROW + (lane & 1) * (ROW / 2) + b)) & 0x7f7f7f7fu;
+            codes |= __shfl_xor_sync(0xffffffffu, codes, 1);
+            const unsigned some = __ballot_sync(0xffffffffu, codes != 0);  // bits 2 c of cells c
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (!((some >> (2 * (pg - w16 + 8 * r))) & 1)) vf[r] = 0u;
+            choose();
+            apart |= __reduce_or_sync(0xffffffffu, (low[0] ? 1u << (pg - w16) : 0u) | (low[1] ? 256u << (pg - w16) : 0u));
+          }
+        }
+        // O^T += V^T P^T
+        uint32_t ph[NC][2], pl[NC][2];  // B fragments of P^T: two f16 terms each
+#pragma unroll
+        for (int n = 0; n < NC; ++n)
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float x = s[n][2 * r] * w[r], y = s[n][2 * r + 1] * w[r];
             const __half2 h = __floats2half2_rn(x, y);
             const float2 back = __half22float2(h);
             ph[n][r] = transpose8x8(as_u32(h));
             pl[n][r] = transpose8x8(as_u32(__floats2half2_rn(x - back.x, y - back.y)));
           }
-        }
-
-        // O^T += V^T P^T
 #pragma unroll
         for (int k = 0; k < KS; ++k) {
           float d[NC][4];
@@ -841,20 +866,17 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
           for (int n = 0; n < NC; ++n)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) acc[k][n][i] += d[n][i];
+            for (int i = 0; i < 4; ++i) acc[k][n][i] = FMT == QSA_PAGE_FP8 ? fmaf(d[n][i], unit, acc[k][n][i]) : acc[k][n][i] + d[n][i];
         }
 
-        if (apart) {  // rows that hold no numbers, to the queries that see them
-          const float inv = FMT == QSA_PAGE_FP8 ? __uint_as_float(0x7f000000u - __float_as_uint(vtop)) : 1.0f;
+        if (apart) {  // rows that hold no numbers, to the queries that see them; rows with far smaller scales
 #pragma unroll
           for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int n = 0; n < NC; ++n)
 #pragma unroll
-              for (int i = 0; i < 2; ++i) {
-                const int late = u0 + pg - w16 + 8 * r - seen;
-                if (late >= 0 && late < T - 1) sm.newest[warp][late][n * 8 + 2 * t + i] = s[n][2 * r + i] * inv;
-              }
+              for (int i = 0; i < 2; ++i)
+                stash[(pg - w16 + 8 * r) * 32 + n * 8 + 2 * t + i] = FMT == QSA_PAGE_FP8 ? s[n][2 * r + i] : s[n][2 * r + i] * kPaTop;
           __syncwarp();
 #pragma unroll 1
           for (int r = 0; r < 16; ++r) {
@@ -875,7 +897,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
                   for (int i = 0; i < 2; ++i)
                     if (late < sm.sees[n * 8 + 2 * t + i])
-                      acc[k][n][2 * h + i] = fmaf(sm.newest[warp][late][n * 8 + 2 * t + i], x, acc[k][n][2 * h + i]);
+                      acc[k][n][2 * h + i] = fmaf(stash[r * 32 + n * 8 + 2 * t + i], x, acc[k][n][2 * h + i]);
               }
           }
         }
@@ -901,7 +923,6 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           sm.l[warp][n * 8 + 2 * t + i] = l[n][i];
         }
       }
-    if (lane == 0) sm.vtop[warp] = FMT == QSA_PAGE_FP8 ? vtop / kPaTop : 1.0f / kPaTop;
     sm100::named_bar_sync(1 + team, kPaThreads);
     const bool complete = tile0 == 0 && tile1 == cur.nt;
     float* const out_part = part + int64_t(2 * cta + (first_segment ? 0 : 1)) * R * (D + 4);
@@ -922,7 +943,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
       const float end = complete ? (L == 0.0f ? 0.0f : 1.0f / L) : 1.0f;
 #pragma unroll
-      for (int w = 0; w < kPaWarps; ++w) sm.m[w][tid] = fw[w] * sm.vtop[w];
+      for (int w = 0; w < kPaWarps; ++w) sm.m[w][tid] = FMT == QSA_PAGE_FP8 ? fw[w] : fw[w] * (1.0f / kPaTop);
       sm.l[0][tid] = end;
       if (!complete) {
         out_part[tid * (D + 4) + D] = M;

@@ -280,6 +280,50 @@ def test_attention_with_large_logits_and_small_or_large_values(fmt):
     p.check(q, *p.attend(q))
 
 
+@pytest.mark.parametrize("size", [1e-2, 1e-3, 1e-4, 1e-5])
+@pytest.mark.parametrize("other", ["zero", "large", "both", "ladder"])
+@pytest.mark.parametrize("fmt,T,hq,dim", [("fp8", 1, 8, 128), ("fp8", 4, 8, 128), ("fp8", 3, 4, 64), ("int4", 1, 8, 128)])
+def test_small_values_beside_rows_of_other_sizes(size, other, fmt, T, hq, dim):
+    """V rows of zeros (whose e4m3 scale is 1), large ones whose keys give them next to no
+    weight, and sizes that fall from row to row do not cost the other rows their precision.
+
+    The logits z are exact (one non-zero dim), so the exponent (z - reference) log2(e) has four
+    roundings and the exponential two units, with a reference within 8 ln(2) of the largest.
+    Two f16 terms of 2^7 p leave 2^-25 of p behind at most, or p itself; for e4m3 relative to a
+    power of two at most 2^8 above the row's scale: 2^-24 of the largest weight."""
+    lens = [120, 9, 40, 2500]
+    p = Pool(lens, fmt, 1, dim, 16, seed=3)
+    n = sum(lens)
+    k, v = np.zeros((n, 1, dim), np.float16), p.rng.standard_normal((n, 1, dim)) * size
+    k[..., 0] = p.rng.integers(-2, 3, (n, 1)) / 4
+    if other == "ladder":
+        v *= np.exp2(-0.75 * (np.arange(n) % 16))[:, None, None]
+    if other in ("zero", "both"):
+        v[p.rng.random(n) < 0.1] = 0
+        v[[3, 123, 132]] = 0
+    if other in ("large", "both"):
+        far = p.rng.random(n) < 0.1
+        far[[5, 125, 135]], far[[0, 120, 129, 169]] = True, False
+        v[far] *= 3000
+        k[far, :, 0] = -60
+    p.append(lens, (k, v.astype(np.float16)))
+    q = np.zeros((len(lens), T, hq, dim), np.float16)
+    q[..., 0] = 8.0
+    out, lse = (x.cpu().numpy().astype(np.float64) for x in p.attend(q, sm_scale=0.25))
+    for i, m in enumerate(lens):
+        kk, vv = p.values(i)
+        want, want_lse, bound, _ = P.attention(q[i], kk, vv, 0.25)
+        for u in range(T):
+            seen = m - T + u + 1
+            z, size_of = kk[:seen, 0, 0] * 8.0 * 0.25, np.abs(vv[:seen, 0])
+            w = np.exp(z - want_lse[u, 0])
+            e = (np.abs(z - z.max()) + 8 * np.log(2) + 1) * 2 * UNIT
+            left = np.minimum(w, w.max() * (2.0 ** -24 if fmt == "fp8" else 2.0 ** -32))
+            tol = (w * e) @ size_of + (w @ e + (seen + 64) * UNIT) * bound[u] + left @ size_of
+            assert (np.abs(out[i, u] - want[u]) <= tol).all(), f"{i} {u}: {np.max(np.abs(out[i, u] - want[u]) / tol):.3g}"
+            assert (np.abs(lse[i, u] - want_lse[u]) <= w @ e + (seen + 64) * UNIT + UNIT * np.abs(want_lse[u])).all()
+
+
 def test_attention_of_constant_rows():
     """Equal keys: every cell has the same weight; equal values come back as they are."""
     p = Pool([1000], "f16", 1, 64, 16)
