@@ -449,6 +449,9 @@ size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, i
  * and lse = -inf. sm_scale 0 means 1/sqrt(head_dim); at most 1e20. f32 softmax and accumulation; values of
  * cells that a query does not see (whatever they hold) do not change its result, and the
  * result of a sequence does not depend on the others of the batch beyond f32 rounding.
+ * An infinite or NaN K value that a query sees makes its results NaN (a logit of -inf has
+ * no weight); such a V value makes that dim of them infinite or NaN, as the sum does in f32
+ * (0 * inf = NaN where the cell's weight is below 2^-32 of the largest).
  * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8, n_seqs up to 65,536. Cells of a page id outside the pool
  * are skipped (QSA_ERR_BAD_INDEX); a length beyond the table counts as the table's
  * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). */

@@ -136,6 +136,12 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
   return d;
 }
+// Two f16 values with the infinities (and NaN) as the largest numbers.
+__device__ __forceinline__ uint32_t finite2(uint32_t a) {
+  uint32_t d;
+  asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(0x7bff7bffu));
+  return d;
+}
 __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -861,6 +867,10 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           }
 #pragma unroll
           for (int n = 0; n < NC; ++n) mma0(d[n], f[0], f[1], f[2], f[3], ph[n][0], ph[n][1]);
+          if constexpr (FMT == QSA_PAGE_F16) {  // an infinity times the second term, 0 or negative, would be NaN
+#pragma unroll
+            for (int i = 0; i < 4; ++i) f[i] = finite2(f[i]);
+          }
 #pragma unroll
           for (int n = 0; n < NC; ++n) mma(d[n], f[0], f[1], f[2], f[3], pl[n][0], pl[n][1]);
 #pragma unroll

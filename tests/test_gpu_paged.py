@@ -454,6 +454,40 @@ def test_what_a_query_does_not_see_does_not_matter(fmt, T):
             assert torch.isnan(out[i, bad:]).any(-1).all()      # those that see them say so
 
 
+@pytest.mark.parametrize("T,n", [(1, 40), (1, 3000), (2, 77), (4, 16), (4, 900)])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_infinite_values_that_a_query_sees(T, n, dim):
+    """An infinite V value makes that dim of the output infinite, a NaN or two infinities that
+    differ make it NaN, whether all of the newest queries see the cell or some; no other dim
+    changes."""
+    p = Pool([n], "f16", 2, dim, 16, seed=n)
+    k, v = p.random_rows([n])
+    v[3, 0, 5], v[n // 2, 0, 6], v[7, 0, 7] = np.inf, -np.inf, np.nan
+    v[1, 0, 8], v[9, 0, 8] = np.inf, -np.inf
+    v[2, 0, 9] = v[11, 0, 9] = np.inf
+    v[n - 1, 0, 10], v[n - 1, 1, 11] = np.inf, -np.inf      # cells that only the last query sees
+    v[n - T, 1, 12] = np.inf                                # and one that all do
+    p.append([n], (k, v))
+    q = _query(p.rng, 1, T, 8, dim)
+    out, lse = (x.cpu().numpy().astype(np.float64)[0] for x in p.attend(q))
+    with np.errstate(invalid="ignore"):
+        for u in range(T):
+            seen = n - T + u + 1
+            kk, vv = p.values(0)
+            for h in range(8):
+                z = kk[:seen, h // 4] @ q[0, u, h].astype(np.float64) / np.sqrt(dim)
+                w = np.exp(z - z.max()) / np.exp(z - z.max()).sum()
+                want = (w[:, None] * vv[:seen, h // 4]).sum(0)
+                fine, got = np.isfinite(want), out[u, h]
+                assert np.array_equal(got[~fine], want[~fine], equal_nan=True), (u, h, got[~fine], want[~fine])
+                depth = (np.abs(kk[:seen, h // 4]) @ np.abs(q[0, u, h].astype(np.float64))).max() / np.sqrt(dim)
+                e = (dim * depth + 8 * (2 * depth + np.log(seen) + 1)) * UNIT
+                bound = (w[:, None] * np.abs(vv[:seen, h // 4])).sum(0)
+                size = np.abs(vv[np.isfinite(vv)]).max()
+                tol = (2 * e + (seen + 64) * UNIT) * bound[fine] + seen * 2.0 ** -32 * size
+                assert (np.abs(got[fine] - want[fine]) <= tol).all()
+
+
 def test_scale_strides_and_no_lse():
     p = Pool([100, 40, 7], "fp8", 2, 64, 32, gap=2)
     p.append([100, 40, 7])
