@@ -376,7 +376,8 @@ qsa_status qsa_verify_drafts(const float* target_probs, int64_t target_stride, c
  *     (1 / amax))) in f32, rounded to nearest even and saturated; an all-zero row has scale 1
  *     (QSA_KV_FP8 up to the last bit of the factors: one division a row instead of two).
  *     Value code * scale. A row that holds an infinity reads back as NaN.
- *   QSA_PAGE_INT4: groups of 32 dims with one f16 scale s = f16(amax * f32(1/7)); code =
+ *   QSA_PAGE_INT4: groups of 32 dims with one f16 scale s = min(f16(amax * f32(1/7)), 9352)
+ *     (so that 7 s is finite: only amax = 65504 comes to more); code =
  *     rint(x * (1 / s)) in f32, clamped to [-7, 7], 0 if s = 0; stored as code + 8 (4 bits).
  *     Byte j < 16 of a group holds dim j in its low and dim j + 16 in its high half. Value
  *     f16(code * s), rounded to nearest even. A group that holds a NaN or an infinity

@@ -29,6 +29,7 @@ def quantise(rows, fmt: str):
     with np.errstate(all="ignore"):
         amax = np.abs(g).max(-1)
         scale = np.where(np.isfinite(amax), amax * (one / np.float32(7.0)), np.float32(np.nan)).astype(np.float16)
+        scale = np.minimum(scale, np.float16(9352))     # the largest f16 that 7 times is one (a NaN stays)
         s = scale.astype(np.float32)[..., None]
         inv = one / s
         codes = np.where(np.isfinite(inv), np.clip(np.rint(g * inv), -7, 7), 0).astype(np.int32) + 8

@@ -4,7 +4,7 @@
 // "KV cacheをQ8_0にしてみる") in its paged form, and a 4-bit one beside it. A row is the
 // head_dim values of one (token, KV head).
 //   e4m3: scale = amax * (1/448), code = e4m3(x * (448 * (1/amax)));
-//   4 bits: per 32 dims s = f16(amax * (1/7)), code = rint(x * (1/s)) in [-7, 7].
+//   4 bits: per 32 dims s = min(f16(amax * (1/7)), 9352), code = rint(x * (1/s)) in [-7, 7].
 // Both calls only move data: a row's 2 * head_dim f16 bytes and its stored bytes. A CTA takes
 // some tokens: it finds their places once (sequence, then page), then every thread moves pieces
 // of K and V rows; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
@@ -134,8 +134,10 @@ __device__ __forceinline__ void store_piece(const Piece& x, char* dst, char* sca
     for (int i = 1; i < 8; ++i) h = __hmax2_nan(h, __habs2(half2_at(x, i)));
     h = __hmax2_nan(h, __shfl_xor_sync(0xffffffffu, h, 1));
     const __half top = __hmax_nan(__low2half(h), __high2half(h));
-    const __half s = __half_as_ushort(top) >= 0x7c00u ? __ushort_as_half(0x7fff)
-                                                      : __float2half_rn(__fmul_rn(__half2float(top), 1.0f / 7.0f));
+    // (at most 9352, the largest f16 that 7 times is one: 65504 / 7 would round up to 9360)
+    const __half s = __half_as_ushort(top) >= 0x7c00u
+                         ? __ushort_as_half(0x7fff)
+                         : __hmin(__float2half_rn(__fmul_rn(__half2float(top), 1.0f / 7.0f)), __float2half_rn(9352.0f));
     const float sf = __half2float(s), inv = sf == 0.0f ? 0.0f : 1.0f / sf;
     // rint(y) + 8 in the low bits of y + (1.5 * 2^23 + 8): the sum rounds to a whole number, to
     // even at ties. |y| is below 7.5 unless the scale lost bits (a subnormal f16): then clamped.

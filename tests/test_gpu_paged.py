@@ -216,6 +216,24 @@ def test_rows_of_a_fused_projection_and_special_values():
         assert int(p.status) == 0
 
 
+def test_4bit_rows_of_the_largest_values_are_finite():
+    """Groups whose largest value is each of f16's, 65504 among them, and attention over those."""
+    n = 0x7c00
+    p = Pool([n], "int4", 1, 64, 256)
+    k, v = np.zeros((n, 1, 64), np.float16), np.zeros((n, 1, 64), np.float16)
+    k[:, 0, 40] = v[:, 0, 3] = np.arange(n, dtype=np.uint16).view(np.float16)
+    v[:, 0, 4] = -v[:, 0, 3]
+    p.append([n], (k, v))
+    back = [torch.empty(n, 1, 64, dtype=torch.float16, device="cuda") for _ in range(2)]
+    p.cache.read(*back, p.table_dev, _i32([0]), _i32([0, n]), status=p.status)
+    for x, want in zip(back, p.values(0)):
+        assert torch.isfinite(x).all() and np.array_equal(x.cpu().numpy().astype(np.float64), want)
+    # every weight is 1 / n
+    q = np.zeros((1, 1, 4, 64), np.float16)
+    out, lse = p.attend(q)
+    p.check(q, out, lse)
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 def test_rows_without_a_place_are_skipped_and_reported(fmt):
     p = Pool([32, 32, 32], fmt, 2, 64, 16)

@@ -28,6 +28,19 @@ def test_quantised_special_rows():
     assert np.isnan(v[0, :32]).all() and np.array_equal(v[0, 32:], np.full(32, float(np.float16(1 / 7)) * 7.0).astype(np.float16))
 
 
+def test_4bit_rows_of_finite_values_are_finite():
+    """Every f16 value as a group's largest, each value within half a step of what it was."""
+    x = np.zeros((0x7c00, 64), np.float16)
+    x[:, 40] = np.arange(0x7c00, dtype=np.uint16).view(np.float16)
+    x[:, 3] = -x[:, 40]
+    codes, scales = P.quantise(x, "int4")
+    v = P.values(codes, scales, "int4")
+    assert np.isfinite(scales).all() and np.isfinite(v).all() and scales.max() == 9352
+    # half a step of the scale, and its and the product's rounding to f16 (of 7 scales: 2^-11 and 2^-24)
+    step = np.maximum(scales.astype(np.float64), 2.0 ** -24)
+    assert (np.abs(v - x.astype(np.float64)) <= 0.5 * step.repeat(32, -1) + np.abs(x.astype(np.float64)) * 2.0 ** -10 + 7 * 2.0 ** -25).all()
+
+
 def test_attention_matches_brute_force_and_masks():
     rng = np.random.default_rng(3)
     q, k, v = rng.standard_normal((3, 4, 8)), rng.standard_normal((6, 2, 8)), rng.standard_normal((6, 2, 8))
