@@ -344,7 +344,8 @@ qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, 
  *                reached (every draft before it accepted);
  *   n_drafts     [n_seqs] i32 or NULL; a value outside [0, max_drafts] is clamped and reported;
  *   uniforms     [n_seqs][max_drafts + 1] f32 in [0, 1): u_0.., and u_last in the last place
- *                whatever n is (a negative number or NaN counts as 0);
+ *                whatever n is. A negative number counts as 0; a NaN u_i rejects its draft, a
+ *                NaN u_last counts as 0;
  *   n_accepted, next_token [n_seqs] i32: the outputs.
  * Probabilities are finite and not negative (weights that are NaN count as 0); they need
  * not sum to 1. status (may be NULL) is a device i32 that gets QSA_ERR_BAD_INDEX, if it was

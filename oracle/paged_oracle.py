@@ -87,7 +87,8 @@ def verify(target, draft, tokens, uniforms):
         if not 0 <= d < vocab:
             break
         q = 1.0 if draft is None else float(draft[m][d])
-        if not float(uniforms[m]) * q < target[m, d]:
+        u = 0.0 if uniforms[m] < 0 else float(uniforms[m])   # a NaN keeps nothing
+        if not u * q < target[m, d]:
             break
         m += 1
     w = target[m].copy()

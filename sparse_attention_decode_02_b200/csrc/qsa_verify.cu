@@ -95,7 +95,8 @@ __global__ void __launch_bounds__(kVfThreads) verify_kernel(VerifyArgs a) {
       kept = false;
       if (!odd) {
         const double q = draft ? (double)draft[i * a.draft_stride + d] : 1.0;
-        kept = (double)u[i] * q < (double)target[i * a.target_stride + d];
+        const float x = u[i];  // (a NaN keeps nothing)
+        kept = (double)(x < 0.0f ? 0.0f : x) * q < (double)target[i * a.target_stride + d];
       }
     }
     const unsigned stop = __ballot_sync(0xffffffffu, !kept), bad = __ballot_sync(0xffffffffu, odd);

@@ -133,6 +133,23 @@ def test_random_numbers_at_and_outside_their_range():
     assert _verify(target, draft, tokens, u) == want
 
 
+@pytest.mark.parametrize("K", [1, 3, 40])
+def test_negative_random_numbers_count_as_zero(K):
+    """A draft whose token the target never gives is not accepted by a negative number either."""
+    rng = np.random.default_rng(K)
+    target, draft, tokens, u = _random(rng, 8, K, 90)
+    at = [0, K - 1, K // 2, 0, K - 1, K // 2, 0, 0]
+    for i in range(8):
+        u[i, :K] = -rng.random(K)
+        target[i, at[i], tokens[i, at[i]]] = 0.0
+    u[6, 0] = -np.inf
+    u[7, 0] = -0.0
+    for d in (draft, None):
+        want = [P.verify(target[i], None if d is None else d[i], tokens[i], u[i]) for i in range(8)]
+        assert [m for m, _ in want] == at
+        assert _verify(target, d, tokens, u) == want
+
+
 def test_acceptance_border_and_zero_probabilities():
     p = np.zeros((5, 2, 40), np.float32)
     q = np.zeros((5, 1, 40), np.float32)

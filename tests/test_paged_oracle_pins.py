@@ -83,3 +83,9 @@ def test_verification_corner_cases():
     assert P.verify(p, None, [7], [0.0, 0.0]) == (0, 0)      # no such token: rejected
     assert P.verify(p, p[:1], [1], [0.5, 0.9]) == (1, 2)
     assert P.verify([[0.1, 0.4, 0.4], [1, 0, 0]], [[0.5, 0.5, 0.5]], [0], [0.9, 0.3]) == (0, 1)  # nothing left: argmax
+
+
+@pytest.mark.parametrize("u", [0.0, -0.0, -1.0, float("-inf"), float("nan")])
+def test_a_draft_the_target_never_gives_is_rejected(u):
+    p = np.array([[0.5, 0.5, 0.0], [0.0, 0.25, 0.75]])
+    assert P.verify(p, [[0.2, 0.2, 0.6]], [2], [u, 0.0]) == (0, 0)
