@@ -334,7 +334,10 @@ qsa_status qsa_rollback_rejected(qsa_ctx* ctx, int32_t layer, int32_t n_drafts, 
  *   m < n, or w_j = p_n(j) if all are accepted: the lowest j with
  *   w_0 + ... + w_j > u_last * (w_0 + ... + w_{vocab-1}); the last j with w_j > 0 if there
  *   is none (u_last >= 1), and the lowest j with the largest p_m(j) if no w_j is positive.
- * Products, differences and sums are taken in 64 bits, in a fixed order.
+ * Products, differences and sums are taken in 64 bits. The order of the sums depends on
+ * n_seqs, vocab and the device alone: the same call gives the same tokens, while a u_last
+ * within the rounding of a partial sum (2^-50 or so) may draw a neighbouring token when the
+ * sequence is verified in a batch of another size.
  *   target_probs [n_seqs][max_drafts + 1][vocab] f32, rows target_stride floats apart;
  *   draft_probs  [n_seqs][max_drafts][vocab] f32, rows draft_stride floats apart, or NULL
  *                for drafts without probabilities (looked up, or the draft model's argmax):

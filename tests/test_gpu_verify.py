@@ -112,6 +112,17 @@ def test_ctas_with_few_or_no_tokens_of_a_row():
             assert list(zip(o[0].tolist(), o[1].tolist())) == want
 
 
+def test_batches_of_any_size_give_a_sequence_the_same_token():
+    """A sequence alone, and in batches that give it 16, 8, 4, 2 and 1 CTAs."""
+    rng = np.random.default_rng(21)
+    target, draft, tokens, u = _random(rng, 330, 1, 6001)
+    want = [P.verify(target[i], draft[i], tokens[i], u[i]) for i in range(330)]
+    for n in (1, 18, 70, 140, 290, 330):
+        for at in sorted({0, (330 - n) // 2, 330 - n}):
+            s = slice(at, at + n)
+            assert _verify(target[s], draft[s], tokens[s], u[s]) == want[s]
+
+
 def test_all_weight_on_one_token():
     V = 70001
     for at in (0, 1, 35000, V - 1):
