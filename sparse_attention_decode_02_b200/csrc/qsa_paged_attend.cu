@@ -68,12 +68,12 @@ struct PaCfg {
   static constexpr int KB = kPaTile * ROW;                 // bytes of a tile's K (V) rows
   static constexpr int SB = kPaTile * SROW;                // and of their scales
   static constexpr int KS = D / 16;                        // MMA k-steps of q.K = m-tiles of P.V
-  // Teams of a CTA (one CTA an SM): three where a thread's sums take up to 32 registers (4-bit
-  // rows: 64), two where they take more or 256-byte rows need the shared memory. One more
-  // warpgroup loads. (100 sequences of up to 8,192, us: two column groups of 128 dims, three teams
-  // 154 against 169 at 4 bits, but 280 against 143 at e4m3, whose rows added one by one take
-  // registers too; three groups of 64-dim e4m3 rows 127 against 123.)
-  static constexpr int TEAMS = KS * NC <= (FMT == QSA_PAGE_INT4 ? 16 : 8) && ROW <= 128 ? 3 : 2;
+  // Teams of a CTA (one CTA an SM): three where a thread's sums take up to 32 registers (e4m3
+  // rows: 48, 4-bit rows: 64), two where they take more or 256-byte rows need the shared memory.
+  // One more warpgroup loads. (100 sequences of up to 8,192, us: two column groups of 128 dims,
+  // three teams 154 against 169 at 4 bits, but 280 against 143 at e4m3, whose rows added one by
+  // one take registers too; three groups of 64-dim e4m3 rows 121 against 131.)
+  static constexpr int TEAMS = KS * NC <= (FMT == QSA_PAGE_INT4 ? 16 : FMT == QSA_PAGE_FP8 ? 12 : 8) && ROW <= 128 ? 3 : 2;
   static constexpr int THREADS = kPaThreads * (TEAMS + 1);
   // registers a thread: at launch, and as the warpgroups split them
   static constexpr int REGS = TEAMS == 3 ? 128 : 168;
@@ -416,8 +416,27 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     p.left -= kPaStart;
     if (p.left <= 0 || ++p.head < Hkv) return;
     p.head = 0;
-    do ++p.seq;
-    while (length(p.seq) == 0);
+    if (++p.seq < a.n_seqs && length(p.seq) == 0) {
+      // empty slots of a batch, maybe many in a row: 256 a round of loads (8,192 of them between two
+      // sequences cost 9 us, and 990 when they were looked at one by one)
+      int found = -1;
+#pragma unroll 1
+      for (int s0 = p.seq + 1; found < 0 && s0 < a.n_seqs; s0 += 256) {
+        int n[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) n[i] = s0 + 32 * i + lane < a.n_seqs ? a.seq_lens[s0 + 32 * i + lane] : 0;
+#pragma unroll
+        for (int i = 7; i >= 0; --i) {
+          const unsigned some = __ballot_sync(0xffffffffu, n[i] > 0);
+          if (some) found = s0 + 32 * i + __ffs(some) - 1;
+        }
+      }
+      p.seq = found < 0 ? a.n_seqs : found;
+    }
+    if (p.seq >= a.n_seqs) {  // (only if the lengths changed meanwhile)
+      p.left = 0;
+      return;
+    }
     start_segment(p);
   };
   const auto next_tile = [&](PaCursor& p) {

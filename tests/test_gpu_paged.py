@@ -559,6 +559,59 @@ def test_large_batches(S, top):
     p.check(q, *p.attend(q))
 
 
+@pytest.mark.parametrize("fmt", ["f16", "int4"])
+@pytest.mark.parametrize("heads,T", [(1, 1), (3, 2)])
+def test_batches_of_mostly_empty_slots(fmt, heads, T):
+    """The few sequences of a large batch, thousands of empty slots before, between and behind them."""
+    S = 20011
+    held = {7: 900, 8: 3, 9: 64, 42: 65, 297: 1, 300: 17, 9000: 2500, 9255: 33, 9256: 200, 9513: 16, 19999: 130}
+    lens = [0] * S
+    for i, n in held.items():
+        lens[i] = n
+    p = Pool(lens, fmt, heads, 64, 16, seed=heads)
+    p.append(lens)
+    q = _query(p.rng, S, T, 2 * heads, 64)
+    out, lse = p.attend(q)
+    assert int(p.status) == 0
+    for i in held:
+        assert_attention(out[i].cpu().numpy().astype(np.float64), lse[i].cpu().numpy().astype(np.float64), q[i], *p.values(i),
+                         what=f"slot {i}")
+    empty = torch.ones(S, dtype=torch.bool, device="cuda")
+    empty[list(held)] = False
+    assert not out[empty].any() and torch.isneginf(lse[empty]).all()
+
+
+def test_runs_of_empty_slots_cost_little():
+    """Two sequences whose border falls inside a team's share, with 8,190 empty slots between them or
+    behind them: the same list of work, so the same bits, and about the same time (looking at
+    the slots one by one took ten times as long)."""
+    c = Q.alloc_paged_kv(64, 16, 4, 128, Q.QSA_PAGE_F16)
+    for t in c.tensors[:2]:
+        t.normal_()
+    S, lens = 8192, (150000, 92000)
+    table = torch.arange(9375, dtype=torch.int32, device="cuda")[None].expand(S, -1).remainder(64).contiguous()
+    q = torch.randn(1, 1, 8, 128, device="cuda").half().expand(S, -1, -1, -1).contiguous()
+    ws = torch.empty(c.workspace_bytes(8), dtype=torch.uint8, device="cuda")
+    got, times = [], []
+    for second in (1, S - 1):
+        n = torch.zeros(S, dtype=torch.int32, device="cuda")
+        n[0], n[second] = lens
+        out, lse = torch.empty(S, 1, 8, 128, device="cuda"), torch.empty(S, 1, 8, device="cuda")
+        best = float("inf")
+        for _ in range(10):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            c.attend(q, table, n, out, ws, lse=lse)
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        times.append(best)
+        got.append((out[[0, second]], lse[[0, second]]))
+        assert int((lse > float("-inf")).any(-1).sum()) == 2
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    assert times[1] < 3 * times[0], times
+
+
 def test_one_very_long_among_short_sequences():
     lens = [1, 0, 30000, 5] + [64] * 30
     p = Pool(lens, "int4", 1, 128, 32, seed=9)
