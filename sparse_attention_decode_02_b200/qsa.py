@@ -396,6 +396,8 @@ class PagedKV:
         if k_pages.dim() != 4:
             raise ValueError("k_pages must be [n_pages, n_kv_heads, page_size, row]")
         n, heads, page, row = k_pages.shape
+        if n < 1:
+            raise QsaError(1, "a paged cache has at least one page")
         self.head_dim = 2 * row if page_format == QSA_PAGE_INT4 else row
         self.n_kv_heads, self.device = heads, k_pages.get_device()
         types = {QSA_PAGE_F16: (_Types.f16,), QSA_PAGE_FP8: (_Types.u8, _Types.e4m3), QSA_PAGE_INT4: (_Types.u8,)}
@@ -428,7 +430,7 @@ class PagedKV:
         self.desc = QsaPagedKv(n, page, heads, self.head_dim, page_format, 0, stride(k_pages, v_pages),
                                stride(k_scales, v_scales), *addr)
         self._ref = ctypes.byref(self.desc)
-        if n < 1 or self.lib.qsa_paged_bytes(self._ref, QSA_PAGED_BUF_PAGES) == 0:
+        if self.lib.qsa_paged_bytes(self._ref, QSA_PAGED_BUF_PAGES) == 0:
             raise QsaError(5, "no such paged cache: page_size 16..256 (a power of two), head_dim 64 or 128")
 
     def _rows(self, k, v, block_table, first, row_start, status):
@@ -488,7 +490,7 @@ class PagedKV:
         if dim != self.head_dim:
             _bad("q", q, _Types.f16, (n_seqs, n_queries, n_q_heads, self.head_dim))
         stride = _rows_stride("q", q, _Types.f16, shape, dev)
-        width = block_table.shape[1]
+        width = block_table.shape[-1]
         if workspace.get_device() != dev or not workspace.is_contiguous():
             raise ValueError("workspace must be contiguous on the current device")
         st = self._attend(

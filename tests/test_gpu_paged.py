@@ -849,6 +849,16 @@ def test_same_inputs_give_the_same_bits():
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+def test_binding_refuses_a_flat_table():
+    p = Pool([64], "f16", 1, 64, 16)
+    q, out = torch.zeros(1, 1, 4, 64, dtype=torch.float16, device="cuda"), torch.zeros(1, 1, 4, 64, device="cuda")
+    ws, rows = torch.zeros(p.cache.workspace_bytes(4), dtype=torch.uint8, device="cuda"), torch.zeros(3, 1, 64, dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        p.cache.attend(q, p.table_dev[0], _i32([1]), out, ws)
+    with pytest.raises(ValueError):
+        p.cache.write(rows, rows, p.table_dev[0], _i32([0]), _i32([0, 3]))
+
+
 def test_binding_refusals():
     p = Pool([64], "fp8", 2, 64, 16)
     q = torch.zeros(1, 1, 4, 64, dtype=torch.float16, device="cuda")

@@ -141,6 +141,13 @@ def test_empty_and_good_verify_arguments(lib):
     assert lib.qsa_rollback_rejected(None, 0, 1, PTR, None) == INVALID
 
 
+def test_binding_refuses_a_cache_without_pages(lib):
+    for fmt, row, kind in ((Q.QSA_PAGE_F16, 64, torch.float16), (Q.QSA_PAGE_FP8, 64, torch.uint8), (Q.QSA_PAGE_INT4, 32, torch.uint8)):
+        pages, scales = torch.zeros(0, 2, 16, row, dtype=kind), torch.zeros(0, 2, 16)
+        with pytest.raises(Q.QsaError):
+            Q.PagedKV(pages, pages, fmt, scales, scales)
+
+
 def test_binding_refuses_tensors_that_are_not_on_the_gpu():
     pages = torch.zeros(4, 2, 16, 64, dtype=torch.float16)
     with pytest.raises(ValueError):
