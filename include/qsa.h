@@ -397,7 +397,8 @@ typedef struct {
   int32_t reserved;      /* 0                                                            */
   int64_t page_stride;   /* bytes from one page to the next in k_pages and v_pages, a
                             multiple of 16; 0: the pages follow one another              */
-  int64_t scale_stride;  /* the same in k_scales and v_scales                            */
+  int64_t scale_stride;  /* the same in k_scales and v_scales. The four buffers are
+                            16-byte aligned, no more is asked of them or of the strides  */
   void* k_pages;         /* [n_pages][n_kv_heads][page_size][head_dim] f16, e4m3 bytes, or
                             [head_dim / 2] bytes of 4-bit codes: a head's rows of a page
                             are one contiguous piece                                     */

@@ -1112,7 +1112,10 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // TMA descriptor of K or V pages as (128-byte lines, a page's lines, pages), or with 128-dim
-// f16 rows (row, a page's rows, pages); a tile holds `rows` rows resp. halves of rows.
+// f16 rows (row, a page's rows, pages); a tile holds `rows` rows resp. halves of rows. The driver
+// API asks for a base address and strides that are multiples of 16 bytes (32 only with
+// interleaving) and, with the 128-byte swizzle, an inner extent of the tile of at most 128
+// bytes; it is the tile in shared memory that lies on 1024 (the pattern), not the pages.
 cudaError_t encode_pages(const PagedView& c, int format, void* pages, int rows, CUtensorMap* out) {
   static const EncodeTiledFn fn = [] {
     void* p = nullptr;

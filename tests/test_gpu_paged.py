@@ -519,6 +519,44 @@ def test_scale_strides_and_no_lse():
     assert torch.equal(a, b) and torch.equal(la, lb) and torch.equal(c, b)
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("offset,gap", [(16, 0), (48, 16), (112, 80), (0, 16)])
+@pytest.mark.parametrize("heads,dim,page", [(1, 64, 16), (3, 128, 32)])
+def test_pages_at_multiples_of_16_bytes(fmt, offset, gap, heads, dim, page):
+    """Pages and scales that start at any multiple of 16 bytes, and lie such multiples apart: equal
+    to the bit to the same pages one after another."""
+    p = Pool([70, 33, 0, 260], fmt, heads, dim, page, seed=dim)
+    lens = [70, 33, 0, 260]
+    parts = []
+    for t in p.parts:
+        if t is None:
+            parts.append(None)
+            continue
+        n, size, each = len(t), t[0].numel(), t.element_size()
+        flat = torch.full((offset // each + n * (size + gap // each) + 64,), 77, dtype=t.dtype, device="cuda")
+        at = flat[offset // each:]
+        assert flat.data_ptr() % 256 == 0 and at.data_ptr() % 256 == offset
+        strides = (size + gap // each,) + t[0].stride()
+        parts.append(at.as_strided(t.shape, strides))
+    other = Q.PagedKV(parts[0], parts[1], FORMATS[fmt], *parts[2:])
+    k, v = p.append(lens)
+    first, start = _i32([0] * 4), _i32(np.concatenate([[0], np.cumsum(lens)]))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    other.write(H.to_dev(k), H.to_dev(v), p.table_dev, first, start, status=status)
+    back = [torch.zeros(sum(lens), heads, dim, dtype=torch.float16, device="cuda") for _ in range(4)]
+    p.cache.read(back[0], back[1], p.table_dev, first, start)
+    other.read(back[2], back[3], p.table_dev, first, start, status=status)
+    assert torch.equal(back[0], back[2]) and torch.equal(back[1], back[3])
+    for T in (1, 3):
+        q = H.to_dev(_query(p.rng, 4, T, 2 * heads, dim))
+        out, lse = p.attend(q)
+        got, got_lse = torch.empty_like(out), torch.empty_like(lse)
+        ws = torch.empty(other.workspace_bytes(2 * heads, T), dtype=torch.uint8, device="cuda")
+        other.attend(q, p.table_dev, _i32(lens), got, ws, lse=got_lse, status=status)
+        assert torch.equal(out, got) and torch.equal(lse, got_lse)
+    assert int(status) == 0 and int(p.status) == 0
+
+
 def test_bad_lengths_and_pages_are_reported():
     p = Pool([64, 64, 64], "f16", 1, 64, 16)
     p.append([64, 64, 64])
