@@ -184,10 +184,10 @@ struct PagedView {
   int n_pages, page_shift, n_kv_heads, head_dim;
 };
 
-inline int page_row_bytes(int format, int head_dim) {
+constexpr int page_row_bytes(int format, int head_dim) {
   return format == QSA_PAGE_F16 ? 2 * head_dim : format == QSA_PAGE_FP8 ? head_dim : head_dim / 2;
 }
-inline int page_scale_bytes(int format, int head_dim) {  // of one row
+constexpr int page_scale_bytes(int format, int head_dim) {  // of one row
   return format == QSA_PAGE_F16 ? 0 : format == QSA_PAGE_FP8 ? 4 : head_dim / 32 * 2;
 }
 

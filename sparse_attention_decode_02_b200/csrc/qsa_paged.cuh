@@ -9,15 +9,14 @@
 
 namespace qsa {
 
-constexpr int kInt4Group = 32;  // dims that share one scale of a 4-bit row
-
+// Bytes of a row and of its scales, as constants.
 template <int FMT>
 __host__ __device__ constexpr int page_row_bytes_c(int d) {
-  return FMT == QSA_PAGE_F16 ? 2 * d : FMT == QSA_PAGE_FP8 ? d : d / 2;
+  return page_row_bytes(FMT, d);
 }
 template <int FMT>
 __host__ __device__ constexpr int page_scale_bytes_c(int d) {
-  return FMT == QSA_PAGE_F16 ? 0 : FMT == QSA_PAGE_FP8 ? 4 : d / kInt4Group * 2;
+  return page_scale_bytes(FMT, d);
 }
 
 // Index of a row in its page: a head's rows of a page are consecutive.
