@@ -506,6 +506,42 @@ def test_infinite_values_that_a_query_sees(T, n, dim):
                 assert (np.abs(got[fine] - want[fine]) <= tol).all()
 
 
+@pytest.mark.parametrize("fmt", ["fp8", "int4"])
+@pytest.mark.parametrize("T,n", [(1, 50), (3, 700), (4, 5000)])
+def test_visible_values_that_are_no_numbers_in_8_and_4_bits(fmt, T, n):
+    """What a stored row reads back as decides: a NaN stays in its dim (e4m3) or its group of 32 (4
+    bits), an infinity takes the row or the group; a K row without numbers takes its head's
+    results. Everything else is as if they were not there."""
+    p = Pool([n, 40], fmt, 3, 64, 16, seed=n)
+    k, v = p.random_rows([n, 40])
+    v[3, 0, 5] = np.nan
+    v[n // 2, 1, 40] = np.inf
+    v[n // 2 + 1] *= 2.0 ** -12
+    k[7, 2, 9] = np.nan
+    p.append([n, 40], (k, v))
+    q = _query(p.rng, 2, T, 6, 64)
+    out, lse = (x.cpu().numpy().astype(np.float64) for x in p.attend(q))
+    lost = [range(5, 6), range(64), range(64)] if fmt == "fp8" else [range(32), range(32, 64), range(64)]
+    for x, (a, b) in ((k, (7, 2)), (v, (3, 0)), (v, (n // 2, 1))):      # the same rows without them
+        x[a, b] = np.where(np.isfinite(x[a, b]), x[a, b], 0)
+    clean = Pool([n, 40], fmt, 3, 64, 16, seed=n)
+    clean.append([n, 40], (k, v))
+    assert np.isnan(lse[0, :, 4:]).all()
+    for i in range(2):
+        kk, vv = p.values(i)
+        for g in range(3):
+            hs = slice(2 * g, 2 * g + 2)
+            gone = list(lost[g]) if i == 0 else []
+            keep = [d for d in range(64) if d not in gone]
+            assert np.isnan(out[i, :, hs][..., gone]).all()
+            if not keep:
+                continue
+            want, want_lse, bound, depth = P.attention(q[i], *clean.values(i))
+            e = (64 * depth + 8 * (np.abs(want_lse) + depth + 1)) * UNIT
+            tol = ((2 * e[..., None] + (n + 64) * UNIT) * bound + n * 2.0 ** -31 * np.abs(clean.values(i)[1]).max())[:, hs]
+            assert (np.abs(out[i, :, hs] - want[:, hs]) <= tol)[..., keep].all(), (i, g)
+
+
 def test_scale_strides_and_no_lse():
     p = Pool([100, 40, 7], "fp8", 2, 64, 32, gap=2)
     p.append([100, 40, 7])
