@@ -818,8 +818,10 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
         // An e4m3 weight is p times the row's scale. So that its two terms keep their bits it enters
         // relative to a power of two next above the largest scale of the 16 rows, by which the
-        // product is scaled back as it is added. Rows with scales of less than 2^-8 of that are
-        // added one by one in f32, after all-zero rows (their scale is 1) are left out.
+        // product is scaled back as it is added. All-zero rows (their scale is 1) are left out, and
+        // where the others' scales lie more than 2^8 apart the rows outside a window of 2^8,
+        // from the top down the first that no more rows lie below than in, are added one by one
+        // in f32 (one such row in every 16 of 126,000: 78 us instead of 46).
         float w[2] = {kPaTop, kPaTop}, unit = 1.0f;
         if constexpr (FMT == QSA_PAGE_FP8) {
           bool low[2];
@@ -845,8 +847,21 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 #pragma unroll
             for (int r = 0; r < 2; ++r)
               if (!((some >> (2 * (pg - w16 + 8 * r))) & 1)) vf[r] = 0u;
-            choose();
-            apart |= __reduce_or_sync(0xffffffffu, (low[0] ? 1u << (pg - w16) : 0u) | (low[1] ? 256u << (pg - w16) : 0u));
+            const unsigned row0 = 1u << (pg - w16), row1 = row0 << 8;
+#pragma unroll 1
+            for (;;) {  // (ends: a window holds at least the largest row that is left)
+              choose();
+              const unsigned below = __reduce_or_sync(0xffffffffu, (low[0] ? row0 : 0u) | (low[1] ? row1 : 0u));
+              const bool in0 = vf[0] != 0u && !low[0], in1 = vf[1] != 0u && !low[1];
+              const unsigned in = __reduce_or_sync(0xffffffffu, (in0 ? row0 : 0u) | (in1 ? row1 : 0u));
+              if (__popc(below) <= __popc(in)) {
+                apart |= below;
+                break;
+              }
+              apart |= in;
+              if (in0) vf[0] = 0u;
+              if (in1) vf[1] = 0u;
+            }
           }
         }
         // O^T += V^T P^T
