@@ -457,7 +457,9 @@ size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, i
  * result of a sequence does not depend on the others of the batch beyond f32 rounding.
  * An infinite or NaN K value that a query sees makes its results NaN (a logit of -inf has
  * no weight); such a V value makes that dim of them infinite or NaN, as the sum does in f32
- * (0 * inf = NaN where the cell's weight is below 2^-32 of the largest).
+ * (0 * inf = NaN where the cell's weight is below 2^-32 of the largest; with an e4m3 or
+ * 4-bit scale that is infinite, which qsa_paged_write stores only where all of the row reads
+ * back NaN, either).
  * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8, n_seqs up to 65,536. Cells of a page id outside the pool
  * are skipped (QSA_ERR_BAD_INDEX); a length beyond the table counts as the table's
  * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). */

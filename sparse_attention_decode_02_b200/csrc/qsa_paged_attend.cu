@@ -818,7 +818,8 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
 
         // An e4m3 weight is p times the row's scale. So that its two terms keep their bits it enters
         // relative to a power of two next above the largest scale of the 16 rows, by which the
-        // product is scaled back as it is added. All-zero rows (their scale is 1) are left out, and
+        // product is scaled back as it is added. All-zero rows (their scale is 1; one that is not
+        // finite makes them NaN) are left out, and
         // where the others' scales lie more than 2^8 apart the rows outside a window of 2^8,
         // from the top down the first that no more rows lie below than in, are added one by one
         // in f32 (one such row in every 16 of 126,000: 78 us instead of 46).
@@ -846,7 +847,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             const unsigned some = __ballot_sync(0xffffffffu, codes != 0);  // bits 2 c of cells c
 #pragma unroll
             for (int r = 0; r < 2; ++r)
-              if (!((some >> (2 * (pg - w16 + 8 * r))) & 1)) vf[r] = 0u;
+              if (!((some >> (2 * (pg - w16 + 8 * r))) & 1) && (vf[r] & 0x7fffffffu) < 0x7f800000u) vf[r] = 0u;
             const unsigned row0 = 1u << (pg - w16), row1 = row0 << 8;
 #pragma unroll 1
             for (;;) {  // (ends: a window holds at least the largest row that is left)

@@ -542,6 +542,30 @@ def test_visible_values_that_are_no_numbers_in_8_and_4_bits(fmt, T, n):
             assert (np.abs(out[i, :, hs] - want[:, hs]) <= tol)[..., keep].all(), (i, g)
 
 
+@pytest.mark.parametrize("scale", [np.inf, -np.inf, np.nan])
+@pytest.mark.parametrize("T,n", [(1, 50), (2, 40), (4, 900)])
+def test_zero_codes_of_a_scale_that_is_no_number(scale, T, n):
+    """e4m3 codes of zero stand for 0 times the row's scale, which is NaN for these scales, in
+    attention as in what is read back, beside rows of any size."""
+    p = Pool([n, n], "fp8", 2, 64, 16, seed=n)
+    k, v = p.random_rows([n, n])
+    v[5::7] *= 2.0 ** -12
+    p.append([n, n], (k, v))
+    page, place = int(p.table[0, 0]), 3
+    p.parts[1][page, 1, place] = 0
+    p.parts[3][page, 1, place] = float(scale)
+    back = torch.empty(n, 2, 64, dtype=torch.float16, device="cuda")
+    p.cache.read(None, back, p.table_dev, _i32([0, 0]), _i32([0, n, n]))
+    assert torch.isnan(back[place, 1]).all() and int(torch.isnan(back).sum()) == 64
+    q = _query(p.rng, 2, T, 4, 64)
+    out, lse = (x.cpu().numpy().astype(np.float64) for x in p.attend(q))
+    assert np.isnan(out[0, :, 2:]).all()
+    for i, hs in ((0, slice(0, 2)), (1, slice(0, 4))):
+        kk, vv = (x[:, : hs.stop // 2] for x in p.values(i))
+        assert_attention(out[i, :, hs], lse[i, :, hs], q[i][:, hs], kk, vv)
+    assert np.isfinite(lse).all()
+
+
 def test_scale_strides_and_no_lse():
     p = Pool([100, 40, 7], "fp8", 2, 64, 32, gap=2)
     p.append([100, 40, 7])
