@@ -462,7 +462,8 @@ size_t qsa_paged_workspace_bytes(const qsa_paged_kv* cache, int32_t n_q_heads, i
  * back NaN, either).
  * n_queries 1..QSA_MAX_QUERIES, n_q_heads / n_kv_heads 1..8, n_seqs up to 65,536. Cells of a page id outside the pool
  * are skipped (QSA_ERR_BAD_INDEX); a length beyond the table counts as the table's
- * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). */
+ * (QSA_ERR_CAPACITY), a negative one as 0 (QSA_ERR_BAD_INDEX). QSA_ERR_TIMEOUT in status: a
+ * wait for a copy inside the kernel gave up, the outputs are not valid. */
 qsa_status qsa_paged_attend(const qsa_paged_kv* cache, const void* q, int64_t q_stride, int32_t n_queries,
                             int32_t n_q_heads, const int32_t* block_table, int32_t table_width, int32_t n_seqs,
                             const int32_t* seq_lens, float sm_scale, float* out, float* lse, void* workspace,
