@@ -9,8 +9,8 @@
 // some tokens: it finds their places once (sequence, then page), then every thread moves pieces
 // of K and V rows; a row's pieces sit in neighbouring lanes, which share its scale by shuffles.
 // Measured on B200 (us; share of a copy's 6,568 GB/s): 61,789 tokens x 4 heads x 128 dims
-// written to f16 pages 41 (95%), to e4m3 33 (88%); 126,253 read from e4m3 65 (92%); 73,000
-// written in 4 bits and read back 67 (70%: the issue slots, in both); 64 tokens 2.7 (latency).
+// written to f16 pages 40 (95%), to e4m3 33 (89%); 126,253 read from e4m3 64 (93%); 58,096
+// written in 4 bits and read back 67 (69%: the issue slots, in both); 64 tokens 2.5 (latency).
 // Pieces of 16 values take fewer instructions a value than 8 (e4m3 writes 38 -> 33, 4-bit
 // 45 -> 35), but a read's stores then leave every other 16 bytes to a second instruction
 // (65 -> 73), so reads take 8. More pieces in flight cost CTAs an SM (registers). Codes are

@@ -18,9 +18,10 @@
 //    tile, with no barrier between warps inside a segment. The products run on the tensor
 //    cores, transposed: S^T = K q^T and O^T = V^T P^T, cells resp. dims as the 16 MMA rows
 //    and the (query, head) rows of the KV head as columns, so that no MMA row is padding.
-//    mma.sync rather than tcgen05: 8 to 32 columns leave the products far from any tensor
-//    bound (the bytes bound this kernel), and 8- and 4-bit rows become f16 operands in
-//    registers, where mma.sync takes them and tcgen05 would want them written back.
+//    mma.sync rather than tcgen05: with one query the bytes bound the f16 and e4m3 forms, and
+//    8- and 4-bit rows become f16 operands in registers, where mma.sync takes them and tcgen05
+//    would want them written back. (Not so for 32 columns over 4-bit rows: there the products
+//    alone take twice as long as the bytes.)
 //  - Precision: codes are exact in f16 (e4m3 scales multiply logits and weights in f32; a 4-bit
 //    value is an f16 product by definition). A weight enters the second product as two f16
 //    terms of 2^7 p (22 bits, down to 2^-32 of the largest), which costs a second MMA and
@@ -34,12 +35,12 @@
 //    at some 50 cycles each, so an unrolled copy of the tile's code for the segment's end, or
 //    a result loop unrolled over the columns, cost 19 us a segment.
 // Measured on B200 (us; share of a copy's 6,568 GB/s over the bytes that must be read): one
-// sequence of 126,253 tokens in f16 47 (84%), 255,181 in e4m3 53 (78%), 128 sequences of up to
-// 8,192 in e4m3 113 (82%): bound by the loads, less some 5 us to start and 4 us to merge. 24
-// sequences of up to 32,768 with four queries each in 4 bits 216 (16%), with one 88 (40%): bound
-// by the instructions that turn codes into operands and weights into fragments, and their
-// latency at 8 to 12 warps an SM (issue slots 48% busy, tensor pipe 35%). A lone sequence of
-// 1,024 tokens 7.9, all latency.
+// sequence of 126,253 tokens in f16 47 (84%), 255,181 in e4m3 52 to 56 (73 to 79%, over several
+// boards), 128 sequences of up to 8,192 in e4m3 109 to 124 (74 to 85%): bound by the loads, less
+// some 5 us to start and 4 us to merge. 24 sequences of up to 32,768 with four queries each in 4
+// bits 203 (17%), with one 87 (40%): bound by the instructions that turn codes into operands and
+// weights into fragments, and their latency at 8 to 12 warps an SM (issue slots 51% busy, tensor
+// pipe 38%). A lone sequence of 1,024 tokens 8.0, all latency.
 #include <atomic>
 
 #include "qsa_paged.cuh"
@@ -822,7 +823,7 @@ paged_attend_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         // finite makes them NaN) are left out, and
         // where the others' scales lie more than 2^8 apart the rows outside a window of 2^8,
         // from the top down the first that no more rows lie below than in, are added one by one
-        // in f32 (one such row in every 16 of 126,000: 78 us instead of 46).
+        // in f32 (one such row in every 16 of 126,000: 80 us instead of 46).
         float w[2] = {kPaTop, kPaTop}, unit = 1.0f;
         if constexpr (FMT == QSA_PAGE_FP8) {
           bool low[2];

@@ -9,8 +9,8 @@
 // summed again to find j: the bytes of one or two rows bound it, and for few sequences the
 // chain token -> its probabilities -> row -> sums -> token. A cluster of CTAs shares a row, as
 // many as fill the GPU; their sums meet in distributed shared memory, so that one launch does.
-// Measured on B200 (us; share of a copy's 6,568 GB/s): 64 sequences x 151,936 tokens 19 (49%),
-// 256 x 100,003 40 (73%), one x 32,000 4.4, one x 151,936 6.8. The small ones are that chain.
+// Measured on B200 (us; share of a copy's 6,568 GB/s): 64 sequences x 151,936 tokens 19 (48%),
+// 256 x 100,003 40 to 42 (70 to 72%), one x 32,000 4.3, one x 151,936 6.8. The small ones are that chain.
 // Sums are f64: among 150,000 weights an f32 sum is off by more than the small weights, and
 // the token would depend on the order.
 #include <atomic>
